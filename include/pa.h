@@ -80,6 +80,9 @@ typedef enum {
                                   (blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z)) */
   PA_DEV_VALUE_RANGE = 6,      /* pa_prefill, bf16 caches: an attended V element with |v| >= 2^24
                                   (outside the kernel's fp16 range for V); detail = sequence */
+  PA_DEV_BAD_POSITION = 7,     /* position >= max_position (pa_rope_and_cache*); detail = the position */
+  PA_DEV_BAD_GROUP = 8,        /* a group's start or prefix out of range (pa_decode_shared_prefix);
+                                  detail = group, -1 for a sequence before the first group */
 } pa_device_error_t;
 
 /*
@@ -121,6 +124,74 @@ pa_status_t pa_reshape_and_cache_fp8(const void *key, const void *value, void *k
                                      const int64_t *slot_mapping, int num_tokens, int64_t num_blocks,
                                      int block_size, int num_kv_heads, int head_dim, pa_dtype_t src_dtype,
                                      float k_scale, float v_scale, void *stream);
+
+/*
+ * pa_rope_table -- cosines and sines of the rotary position embedding.  The
+ * pages have no counterpart to this call and the next two: their sketch leaves
+ * positions out of the attention, and the models they serve rotate q and k by
+ * position before the cache write.
+ *
+ * cos_sin       [max_position][rotary_dim] fp32 (written): row p holds
+ *               cos(p * base^(-2i/rotary_dim)) for i < rotary_dim / 2, then the
+ *               sines.  Angles, cosines and sines are computed in fp64 and
+ *               rounded once.  16-byte aligned.
+ * Errors: PA_ERR_NULL, PA_ERR_SHAPE (max_position <= 0, rotary_dim odd or <= 0,
+ * base not finite or <= 0), PA_ERR_ALIGN, PA_ERR_CUDA.
+ */
+pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, double base, void *stream);
+
+/*
+ * pa_rope_and_cache -- pa_reshape_and_cache with the position rotation applied
+ * on the way: rotates each token's q rows into q_out and its K rows into the
+ * cache, and writes its V rows to the cache, in one launch.
+ *
+ * q             [num_tokens] rows of num_heads * head_dim elements, q_stride
+ *               elements apart (heads contiguous in a row), so that q, key and
+ *               value may be slices of one projection's output; key, value
+ *               likewise with num_kv_heads; q_out likewise.  All in dtype.
+ *               q_out may be q itself (same pointer and stride: rotated in
+ *               place); otherwise it must not overlap q, key or value.
+ * positions     [num_tokens] int64.  A token with position < 0 is padding: none
+ *               of its rows is read or written.  position >= max_position: the
+ *               token is skipped and recorded as PA_DEV_BAD_POSITION.
+ * cos_sin       [max_position][rotary_dim] fp32 (pa_rope_table, or the caller's).
+ * slot_mapping  [num_tokens] int64 as in pa_reshape_and_cache: slot < 0 writes no
+ *               cache row (q is still rotated), a slot past the pool is
+ *               recorded as PA_DEV_BAD_SLOT (q is still rotated).
+ * interleaved   0: the pair of element i < rotary_dim / 2 is (i, i +
+ *               rotary_dim / 2); otherwise it is (2i, 2i + 1).
+ * With a pair (a, b) and its cos c and sin s: a' = a c - b s, b' = b c + a s, each
+ * product and sum rounded to fp32, then rounded to dtype (nearest even).
+ * Elements from rotary_dim on, and V, are copied bit for bit.
+ * Errors: PA_ERR_NULL, PA_ERR_DTYPE, PA_ERR_SHAPE (as pa_reshape_and_cache;
+ * rotary_dim not a multiple of 16 (fp32: 8) or > head_dim; a stride below the
+ * row or above 2^31 - 1; max_position <= 0; q_out overlapping), PA_ERR_ALIGN (16
+ * bytes for every tensor but positions and slot_mapping (8), strides multiples
+ * of 16 bytes), PA_ERR_CUDA.  num_tokens == 0 is a no-op.
+ */
+pa_status_t pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                              void *v_cache, const int64_t *positions, const float *cos_sin,
+                              const int64_t *slot_mapping, int num_tokens, int64_t q_out_stride, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int max_position, int rotary_dim, int interleaved,
+                              int64_t num_blocks, int block_size, int num_heads, int num_kv_heads, int head_dim,
+                              pa_dtype_t dtype, void *stream);
+
+/*
+ * pa_rope_and_cache_fp8 -- pa_rope_and_cache into 1-byte E4M3 caches.
+ *
+ * q, q_out, key, value in src_dtype (PA_F16 or PA_BF16), head_dim 128.  A rotated K
+ * element is quantised from its fp32 value (it is not rounded to src_dtype
+ * first): the E4M3 code nearest to the fp32 quotient by k_scale, as
+ * pa_reshape_and_cache_fp8; V with v_scale.  Everything else as
+ * pa_rope_and_cache; PA_ERR_SHAPE also for a scale that is not finite and > 0.
+ */
+pa_status_t pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                                  void *v_cache, const int64_t *positions, const float *cos_sin,
+                                  const int64_t *slot_mapping, int num_tokens, int64_t q_out_stride, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, int max_position, int rotary_dim,
+                                  int interleaved, int64_t num_blocks, int block_size, int num_heads,
+                                  int num_kv_heads, int head_dim, pa_dtype_t src_dtype, float k_scale, float v_scale,
+                                  void *stream);
 
 /*
  * pa_decode_partition_size -- the partition size (tokens per split-K piece)
@@ -257,6 +328,130 @@ pa_status_t pa_prefill(void *out, const void *q, const void *k_cache, const void
                        pa_dtype_t dtype, void *stream);
 
 /*
+ * pa_decode_shared_prefix_workspace_bytes -- bytes of workspace that
+ * pa_decode_shared_prefix needs for these arguments on the current device (0 for
+ * invalid arguments and for num_seqs == 0).
+ */
+size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
+                                               int head_dim, int max_prefix_len, int max_suffix_len,
+                                               int max_group_size);
+
+/*
+ * pa_decode_shared_prefix -- pa_decode for batches whose sequences share long
+ * prefixes ([A] §三 share_prefix: several block tables start with the same
+ * physical blocks): the attention of a group's queries to the prefix is
+ * computed once for all of them on the 5th-generation tensor cores, that to
+ * each sequence's own tokens as in pa_decode, and the two are combined.  The
+ * result is pa_decode's on the same arguments up to rounding.
+ *
+ * group_start   [num_groups + 1] int32, non-decreasing from 0 to num_seqs:
+ *               sequences group_start[i] .. group_start[i+1] - 1 form group i.
+ * prefix_lens   [num_groups] int32, multiples of 16: the first prefix_lens[i]
+ *               tokens of every sequence of group i are the same.  Their blocks
+ *               are read from the table row of the group's first sequence; the
+ *               other rows' entries for them are not read.  0: nothing shared.
+ * context_lens  [num_seqs] int32 whole lengths, prefix included; each must be >=
+ *               its group's prefix and at most max_suffix_len tokens longer
+ *               (else PA_DEV_BAD_CONTEXT_LEN and that row is not written).
+ *               A row without any token (length 0) is all zeros.
+ * max_prefix_len (a multiple of 16), max_suffix_len, max_group_size
+ *               host-side upper bounds; they size the grid and the workspace.
+ *               A group whose entries exceed them or the tables is recorded as
+ *               PA_DEV_BAD_GROUP and its rows are not written.
+ * scale         finite and > 0.
+ * workspace     pa_decode_shared_prefix_workspace_bytes(...) bytes, 256-byte
+ *               aligned; scratch.  Calls that overlap on the GPU need one each.
+ * dtype PA_F16 or PA_BF16, head_dim 128, group size (num_heads / num_kv_heads) 1,
+ * 2, 4 or 8.  Accumulation is fp32; softmax weights enter the prefix's P V as
+ * fp16 (relative rounding 2^-11, PA_F16) or as two bf16 parts (2^-17, PA_BF16).
+ * Bad block ids of a prefix read as zeros (PA_DEV_BAD_BLOCK_ID).
+ * Errors: as pa_decode, PA_ERR_DTYPE for other types, PA_ERR_SHAPE also for
+ * num_seqs > 0 without groups and a max_prefix_len off 16.
+ */
+pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                    const int32_t *group_start, const int32_t *prefix_lens, int num_seqs,
+                                    int num_groups, int num_heads, int max_prefix_len, int max_suffix_len,
+                                    int max_group_size, float scale, void *workspace, size_t workspace_bytes,
+                                    int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                    pa_dtype_t dtype, void *stream);
+
+/*
+ * Block-sparse decode: three calls that attend to the blocks of a long context
+ * that matter to a query.  The pages have no counterpart to them.
+ *
+ * pa_update_block_bounds -- after new tokens were written (pa_reshape_and_cache,
+ * pa_rope_and_cache): the per-channel smallest and largest key of every block
+ * that holds one of a sequence's last new_lens[b] tokens, from all of that block's
+ * tokens before context_lens[b].
+ *
+ * block_bounds  [num_blocks][2][num_kv_heads][head_dim], cache dtype: [0] the
+ *               smallest, [1] the largest; exact.  A NaN key gives NaN.  Other
+ *               blocks' entries are not touched.
+ * new_lens      [num_seqs] int32, 0 <= new_lens[b] <= context_lens[b] and <=
+ *               max_new_len (else PA_DEV_BAD_CONTEXT_LEN, sequence skipped).
+ * Sequences that share one of these blocks must agree on how many of its tokens
+ * there are (a shared block is full).
+ * Errors: PA_ERR_NULL, PA_ERR_DTYPE (also PA_FP8_E4M3), PA_ERR_SHAPE,
+ * PA_ERR_ALIGN, PA_ERR_CUDA.  num_seqs == 0 or max_new_len == 0 is a no-op.
+ */
+pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *context_lens, const int32_t *new_lens,
+                                   int num_seqs, int max_new_len, int64_t num_blocks, int block_size,
+                                   int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream);
+
+/* pa_select_blocks_workspace_bytes -- bytes of workspace of pa_select_blocks (0 when it needs none). */
+size_t pa_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len);
+
+/*
+ * pa_select_blocks -- for each sequence b and KV head g, the num_selected of its
+ * n = ceil(context_lens[b] / 16) blocks to attend to: the first sink_blocks, the
+ * last recent_blocks, and of the others those with the largest score
+ *   max_h sum_d (q[b][h][d] >= 0 ? q[b][h][d] * largest[d] : q[b][h][d] * smallest[d])
+ * over the query heads h of the KV head, an upper bound of every q . K_t of the
+ * block.  Scores are fp64; equal ones go to the lowest block; a NaN score counts
+ * as the largest.
+ *
+ * selected      [num_seqs][num_kv_heads][num_selected] int32 (written): logical
+ *               block indices in ascending order, -1 behind them when n <
+ *               num_selected.  A bad context length gives a list of -1.
+ * block_bounds  as pa_update_block_bounds left them for every block of the context.
+ * max_context_len  host-side upper bound of context_lens.
+ * Errors: PA_ERR_NULL, PA_ERR_DTYPE, PA_ERR_SHAPE (as pa_decode; num_selected <=
+ * 0; sink_blocks + recent_blocks > num_selected), PA_ERR_WORKSPACE, PA_ERR_ALIGN,
+ * PA_ERR_CUDA.
+ */
+pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block_bounds, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                             int max_context_len, int num_selected, int sink_blocks, int recent_blocks,
+                             void *workspace, size_t workspace_bytes, int64_t num_blocks, int block_size,
+                             int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream);
+
+/* pa_decode_selected_workspace_bytes -- bytes of workspace of pa_decode_selected on the current device
+ * (0 when it needs none). */
+size_t pa_decode_selected_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                          int num_selected);
+
+/*
+ * pa_decode_selected -- pa_decode over the tokens of the listed blocks only.
+ *
+ * selected      [num_seqs][num_kv_heads][num_selected] int32 logical block
+ *               indices (pa_select_blocks, or the caller's), distinct, in any
+ *               order; an entry < 0 names no block.  Of a sequence's last block
+ *               the tokens before context_lens[b] count.  An entry past the
+ *               sequence's blocks is skipped and recorded as
+ *               PA_DEV_BAD_BLOCK_ID (detail = the entry), a bad table entry
+ *               likewise (detail = the id).
+ * A row whose list names no block is all zeros.  dtype PA_F32, PA_F16 or PA_BF16.
+ * Other arguments, results and errors as pa_decode.
+ */
+pa_status_t pa_decode_selected(void *out, const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                               const int32_t *selected, int num_seqs, int num_heads, int num_selected, float scale,
+                               void *workspace, size_t workspace_bytes, int64_t num_blocks, int block_size,
+                               int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream);
+
+/*
  * pa_copy_blocks -- copy-on-write block copies ([B] Block 管理器, item 3:
  * when a request writes to a block that several requests share, the block is
  * copied first and the request's table is pointed at the copy; the caller
@@ -351,8 +546,9 @@ pa_status_t pa_stream_read(const void *buf, size_t bytes, uint64_t *sink, void *
  * counterpart on the source pages; ordinary callers never need it).
  *
  * Arms a one-shot flag in the host library: the next launch of `kernel`
- * (0 = the decode partition kernel of any pa_decode* call, 1 = pa_prefill),
- * from any thread, carries it and clears it.  In that launch, CTA `cta` (the
+ * (0 = the decode partition kernel of pa_decode, pa_decode_append,
+ * pa_decode_static_workspace or pa_decode_fp8, 1 = pa_prefill, 3 = the prefix
+ * kernel of pa_decode_shared_prefix), from any thread, carries it and clears it.  In that launch, CTA `cta` (the
  * linear index of PA_DEV_WAIT_TIMEOUT) leaves one of its tile copies unissued
  * -- no copy and no barrier arrival, so nothing is in flight for it -- and its
  * waits give up after 1 ms instead of 2 s.  Its wait on the missing tile runs

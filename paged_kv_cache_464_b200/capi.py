@@ -41,6 +41,27 @@ _lib.pa_decode_fp8.argtypes = [_P, _P, _P, _P, _F, _F, _P, _I, _P, _I, _I, _I, _
                                _P]
 _lib.pa_prefill.restype = _I
 _lib.pa_prefill.argtypes = [_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _I64, _I, _I, _I, _I, _P]
+_D = ctypes.c_double
+_lib.pa_rope_table.restype = _I
+_lib.pa_rope_table.argtypes = [_P, _I, _I, _D, _P]
+_lib.pa_rope_and_cache.restype = _I
+_lib.pa_rope_and_cache.argtypes = [_P] * 9 + [_I] + [_I64] * 4 + [_I, _I, _I, _I64, _I, _I, _I, _I, _I, _P]
+_lib.pa_rope_and_cache_fp8.restype = _I
+_lib.pa_rope_and_cache_fp8.argtypes = [_P] * 9 + [_I] + [_I64] * 4 + [_I, _I, _I, _I64, _I, _I, _I, _I, _I, _F, _F, _P]
+_lib.pa_decode_shared_prefix_workspace_bytes.restype = _SZ
+_lib.pa_decode_shared_prefix_workspace_bytes.argtypes = [_I] * 8
+_lib.pa_decode_shared_prefix.restype = _I
+_lib.pa_decode_shared_prefix.argtypes = [_P] * 5 + [_I] + [_P] * 3 + [_I] * 6 + [_F, _P, _SZ, _I64, _I, _I, _I, _I, _P]
+_lib.pa_update_block_bounds.restype = _I
+_lib.pa_update_block_bounds.argtypes = [_P] * 3 + [_I] + [_P] * 2 + [_I, _I, _I64, _I, _I, _I, _I, _P]
+_lib.pa_select_blocks_workspace_bytes.restype = _SZ
+_lib.pa_select_blocks_workspace_bytes.argtypes = [_I] * 3
+_lib.pa_select_blocks.restype = _I
+_lib.pa_select_blocks.argtypes = [_P] * 4 + [_I, _P] + [_I] * 6 + [_P, _SZ, _I64, _I, _I, _I, _I, _P]
+_lib.pa_decode_selected_workspace_bytes.restype = _SZ
+_lib.pa_decode_selected_workspace_bytes.argtypes = [_I] * 5
+_lib.pa_decode_selected.restype = _I
+_lib.pa_decode_selected.argtypes = [_P] * 5 + [_I] + [_P] * 2 + [_I] * 3 + [_F, _P, _SZ, _I64, _I, _I, _I, _I, _P]
 _lib.pa_copy_blocks.restype = _I
 _lib.pa_copy_blocks.argtypes = [_P, _P, _P, _I, _I64, _I, _I, _I, _I, _P]
 _lib.pa_stream_read.restype = _I
@@ -54,6 +75,9 @@ _lib.pa_status_string.argtypes = [_I]
 
 EXPORTED = ["pa_reshape_and_cache", "pa_decode_partition_size", "pa_decode_workspace_bytes", "pa_decode",
             "pa_decode_append", "pa_decode_static_workspace", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_prefill",
+            "pa_rope_table", "pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_decode_shared_prefix_workspace_bytes",
+            "pa_decode_shared_prefix", "pa_update_block_bounds", "pa_select_blocks_workspace_bytes",
+            "pa_select_blocks", "pa_decode_selected_workspace_bytes", "pa_decode_selected",
             "pa_copy_blocks", "pa_stream_read", "pa_test_stall_next_launch", "pa_get_device_error", "pa_status_string"]
 MAX_COPY_PAIRS = 65536       # PA_MAX_COPY_PAIRS in include/pa.h
 STATIC_WORKSPACE_BYTES = 64 << 20   # PA_STATIC_WORKSPACE_BYTES in include/pa.h
@@ -62,7 +86,8 @@ DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 FP8 = 3                      # PA_FP8_E4M3: 1-byte caches held as torch.uint8 or torch.float8_e4m3fn
 FP8_TORCH = (torch.uint8, torch.float8_e4m3fn)
 DEVICE_ERRORS = {0: "ok", 1: "block id out of range", 2: "slot out of range", 3: "copy pair conflict",
-                 4: "bad context length", 5: "wait timeout"}
+                 4: "bad context length", 5: "wait timeout", 6: "V element out of range", 7: "position out of range",
+                 8: "bad prefix group"}
 
 
 class PaError(RuntimeError):
@@ -317,6 +342,303 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block
     return out
 
 
+# -- rotate and append, shared-prefix decode, block-sparse decode
+# These wrappers run on the tensors' device (which need not be the current one)
+# and allocate what the caller left out on the stream that the call runs on.
+
+def _one_device(**tensors: torch.Tensor) -> torch.device:
+    device = None
+    for name, t in tensors.items():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    return device
+
+
+def _flat(**tensors: torch.Tensor) -> None:
+    for name, t in tensors.items():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(fn, where: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s.cuda_stream)
+    _check(status, where)
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _bytes_of(fn, device: torch.device, *args: int) -> int:
+    """A workspace size, which may depend on the device's SM count."""
+    if device.index == torch.cuda.current_device():
+        return int(fn(*args))
+    with torch.cuda.device(device):
+        return int(fn(*args))
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device,
+               stream: Optional[torch.cuda.Stream]):
+    """(tensor, pointer, bytes); the tensor has to live until the launch is queued."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _empty(need, torch.uint8, device, stream)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the other tensors' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0,
+               device: Optional[torch.device] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """[max_position, rotary_dim] float32: cosines, then sines, of position * base^(-2i / rotary_dim)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    table = _empty((max(max_position, 0), max(rotary_dim, 0)), torch.float32, device, stream)
+    _launch(_lib.pa_rope_table, "pa_rope_table", device, stream, table.data_ptr(), max_position, rotary_dim, float(base))
+    return table
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the token rows of [T, heads, D]; heads and D must be contiguous."""
+    T, h, d = t.shape
+    if T == 0:
+        return h * d
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+def _rope(fn, where, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping, q_out, interleaved, stream,
+          dtype_code, *scales):
+    nb, bs, hkv, d, _ = _cache_args(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [T, num_heads, head_dim]")
+    T, hq, _ = q.shape
+    if key.dtype != q.dtype or value.dtype != q.dtype:
+        raise ValueError("q, key and value must have one dtype")
+    if tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
+        raise ValueError("key/value must be [T, num_kv_heads, head_dim]")
+    if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or positions.numel() != T or \
+            slot_mapping.numel() != T:
+        raise ValueError("positions and slot_mapping must be int64 [T]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rotary_dim] float32")
+    device = _one_device(q=q, key=key, value=value, positions=positions, cos_sin=cos_sin, k_cache=k_cache,
+                         v_cache=v_cache, slot_mapping=slot_mapping)
+    _flat(positions=positions, cos_sin=cos_sin, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
+    if q_out is None:
+        q_out = _empty((T, hq, d), q.dtype, device, stream)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != device:
+        raise ValueError("q_out must match q")
+    _launch(fn, where, device, stream, q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), slot_mapping.data_ptr(), T,
+            _row_stride(q_out, "q_out"), _row_stride(q, "q"), _row_stride(key, "key"), _row_stride(value, "value"),
+            cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, nb, bs, hq, hkv, d, dtype_code, *scales)
+    return q_out
+
+
+def rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                   cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                   q_out: Optional[torch.Tensor] = None, *, interleaved: bool = False,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rotate q [T, Hq, D] into ``q_out`` (q itself: in place) and key [T, Hkv, D] into the cache by ``positions`` [T]
+    (int64; < 0 = padding, nothing done), and write value, at ``slot_mapping`` [T] (int64; < 0 = no cache write).
+    q, key, value and q_out may be slices of wider rows.  ``cos_sin``: ``rope_table``'s."""
+    if k_cache.dtype not in DTYPE_CODE or q.dtype != k_cache.dtype:
+        raise ValueError("q, key and value must have the cache dtype")
+    return _rope(_lib.pa_rope_and_cache, "pa_rope_and_cache", q, key, value, positions, cos_sin, k_cache, v_cache,
+                 slot_mapping, q_out, interleaved, stream, DTYPE_CODE[q.dtype])
+
+
+def rope_and_cache_fp8(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                       cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       slot_mapping: torch.Tensor, k_scale: float, v_scale: float,
+                       q_out: Optional[torch.Tensor] = None, *, interleaved: bool = False,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``rope_and_cache`` from fp16/bf16 rows into 1-byte E4M3 caches."""
+    if k_cache.dtype not in FP8_TORCH or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("1-byte caches and fp16/bf16 q, key and value expected")
+    return _rope(_lib.pa_rope_and_cache_fp8, "pa_rope_and_cache_fp8", q, key, value, positions, cos_sin, k_cache,
+                 v_cache, slot_mapping, q_out, interleaved, stream, DTYPE_CODE[q.dtype], float(k_scale), float(v_scale))
+
+
+def _decode_inputs(q, block_tables, context_lens, d: int, dtype: torch.dtype):
+    S, hq, dq = q.shape
+    if dq != d or q.dtype != dtype:
+        raise ValueError("q must be [S, num_heads, head_dim] with the cache dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.numel() != S:
+        raise ValueError("block_tables must be [S, max_blocks_per_seq] and context_lens [S]")
+    return S, hq
+
+
+def _out_like(q, out, device, stream):
+    if out is None:
+        return _empty(q.shape, q.dtype, device, stream)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != device or not out.is_contiguous():
+        raise ValueError("out must match q and be contiguous")
+    return out
+
+
+def decode_shared_prefix_workspace_bytes(num_seqs: int, num_groups: int, num_heads: int, num_kv_heads: int,
+                                         head_dim: int, max_prefix_len: int, max_suffix_len: int,
+                                         max_group_size: int) -> int:
+    return int(_lib.pa_decode_shared_prefix_workspace_bytes(num_seqs, num_groups, num_heads, num_kv_heads, head_dim,
+                                                            max_prefix_len, max_suffix_len, max_group_size))
+
+
+def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, group_start: torch.Tensor, prefix_lens: torch.Tensor,
+                         scale: float, out: Optional[torch.Tensor] = None, *, max_prefix_len: Optional[int] = None,
+                         max_suffix_len: Optional[int] = None, max_group_size: Optional[int] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Paged decode for groups of sequences with common prefixes.  Sequences group_start[i]:group_start[i+1]
+    (int32 [G + 1]) share their first prefix_lens[i] (int32 [G], multiples of 16) tokens; context_lens are whole
+    lengths.  Callers that know the three maxima should pass them (reading them costs a device-to-host sync)."""
+    nb, bs, hkv, d, dt = _cache_args(k_cache, v_cache)
+    S, hq = _decode_inputs(q, block_tables, context_lens, d, k_cache.dtype)
+    n = prefix_lens.numel()
+    if group_start.dtype != torch.int32 or prefix_lens.dtype != torch.int32 or group_start.numel() != n + 1:
+        raise ValueError("group_start and prefix_lens must be int32 [G + 1] and [G]")
+    device = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                         group_start=group_start, prefix_lens=prefix_lens)
+    _flat(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+          group_start=group_start, prefix_lens=prefix_lens)
+    if max_prefix_len is None or max_suffix_len is None or max_group_size is None:
+        starts, prefixes = group_start.cpu().long(), prefix_lens.cpu().long()
+        sizes = (starts[1:] - starts[:-1]).clamp(min=0)
+        if max_group_size is None:
+            max_group_size = int(sizes.max()) if n else 0
+        if max_prefix_len is None:
+            max_prefix_len = int(prefixes.max()) if n else 0
+        if max_suffix_len is None:
+            own = context_lens.cpu().long()
+            if int(sizes.sum()) == S:
+                own = own - prefixes.repeat_interleave(sizes)
+            max_suffix_len = max(0, int(own.max())) if S else 0
+    out = _out_like(q, out, device, stream)
+    need = 0
+    if workspace is None:
+        need = _bytes_of(_lib.pa_decode_shared_prefix_workspace_bytes, device, S, n, hq, hkv, d, max_prefix_len,
+                         max_suffix_len, max_group_size)
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
+    _launch(_lib.pa_decode_shared_prefix, "pa_decode_shared_prefix", device, stream, out.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), group_start.data_ptr(), prefix_lens.data_ptr(), S, n, hq, max_prefix_len,
+            max_suffix_len, max_group_size, float(scale), ws_ptr, ws_bytes, nb, bs, hkv, d, dt)
+    return out
+
+
+def _bounds_args(block_bounds, nb, hkv, d, dtype):
+    if tuple(block_bounds.shape) != (nb, 2, hkv, d) or block_bounds.dtype != dtype:
+        raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim] with the cache dtype")
+
+
+def update_block_bounds(k_cache: torch.Tensor, block_bounds: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, new_lens: torch.Tensor, *, max_new_len: Optional[int] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Smallest and largest key per channel, ``block_bounds`` [NB, 2, Hkv, D], of every block that holds one of a
+    sequence's last ``new_lens`` (int32 [S]) tokens."""
+    nb, bs, hkv, d, dt = _cache_args(k_cache, k_cache)
+    _bounds_args(block_bounds, nb, hkv, d, k_cache.dtype)
+    S = context_lens.numel()
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or new_lens.dtype != torch.int32:
+        raise ValueError("block_tables, context_lens and new_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or new_lens.numel() != S:
+        raise ValueError("block_tables must be [S, max_blocks_per_seq], context_lens and new_lens [S]")
+    device = _one_device(k_cache=k_cache, block_bounds=block_bounds, block_tables=block_tables,
+                         context_lens=context_lens, new_lens=new_lens)
+    _flat(k_cache=k_cache, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens,
+          new_lens=new_lens)
+    if max_new_len is None:
+        max_new_len = int(new_lens.max()) if S else 0
+    _launch(_lib.pa_update_block_bounds, "pa_update_block_bounds", device, stream, k_cache.data_ptr(),
+            block_bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            new_lens.data_ptr(), S, max_new_len, nb, bs, hkv, d, dt)
+
+
+def select_blocks_workspace_bytes(num_seqs: int, num_kv_heads: int, max_context_len: int) -> int:
+    return int(_lib.pa_select_blocks_workspace_bytes(num_seqs, num_kv_heads, max_context_len))
+
+
+def select_blocks(q: torch.Tensor, block_bounds: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, selected, *, sink_blocks: int = 1, recent_blocks: int = 1,
+                  max_context_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The blocks each (sequence, KV head) attends to, by the score of ``block_bounds``: ``selected`` is the int32
+    [S, Hkv, K] tensor to write, or K.  Ascending logical indices, -1 behind them."""
+    if block_bounds.dim() != 4 or block_bounds.shape[1] != 2 or block_bounds.dtype not in DTYPE_CODE:
+        raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim]")
+    nb, _, hkv, d = block_bounds.shape
+    S, hq = _decode_inputs(q, block_tables, context_lens, d, block_bounds.dtype)
+    device = _one_device(q=q, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens)
+    _flat(q=q, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens)
+    if isinstance(selected, int):
+        selected = _empty((S, hkv, max(selected, 0)), torch.int32, device, stream)
+    elif selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, hkv) or \
+            selected.device != device or not selected.is_contiguous():
+        raise ValueError("selected must be a contiguous int32 [S, num_kv_heads, K]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    need = _lib.pa_select_blocks_workspace_bytes(S, hkv, max_context_len) if workspace is None else 0
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
+    _launch(_lib.pa_select_blocks, "pa_select_blocks", device, stream, selected.data_ptr(), q.data_ptr(),
+            block_bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq,
+            max_context_len, selected.shape[2], sink_blocks, recent_blocks, ws_ptr, ws_bytes, nb, 16, hkv, d,
+            DTYPE_CODE[q.dtype])
+    return selected
+
+
+def decode_selected_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                    num_selected: int) -> int:
+    return int(_lib.pa_decode_selected_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, num_selected))
+
+
+def decode_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, selected: torch.Tensor, scale: float,
+                    out: Optional[torch.Tensor] = None, *, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Paged decode over the blocks of ``selected`` (int32 [S, Hkv, K] distinct logical indices, < 0 = none) only."""
+    nb, bs, hkv, d, dt = _cache_args(k_cache, v_cache)
+    S, hq = _decode_inputs(q, block_tables, context_lens, d, k_cache.dtype)
+    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, hkv):
+        raise ValueError("selected must be int32 [S, num_kv_heads, K]")
+    K = selected.shape[2]
+    device = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                         selected=selected)
+    _flat(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+          selected=selected)
+    out = _out_like(q, out, device, stream)
+    need = 0
+    if workspace is None:
+        need = _bytes_of(_lib.pa_decode_selected_workspace_bytes, device, S, hq, hkv, d, K)
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
+    _launch(_lib.pa_decode_selected, "pa_decode_selected", device, stream, out.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            context_lens.data_ptr(), selected.data_ptr(), S, hq, K, float(scale), ws_ptr, ws_bytes, nb, bs, hkv, d, dt)
+    return out
+
+
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_mapping: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """Copy whole blocks (src, dst) = block_mapping[i] ([P, 2] int64) in both caches."""
@@ -342,8 +664,8 @@ def test_stall_next_launch(kernel: str, cta: int) -> None:
     """Test hook: the next launch of ``kernel`` ("decode" or "prefill") leaves
     one copy of CTA ``cta`` unissued, so that CTA's bounded wait runs out
     (PA_DEV_WAIT_TIMEOUT, detail = cta) within about a millisecond; ``cta=-1``
-    disarms."""
-    _check(_lib.pa_test_stall_next_launch({"decode": 0, "prefill": 1}[kernel], int(cta)),
+    disarms.  "shared_prefix": the prefix kernel of ``decode_shared_prefix``."""
+    _check(_lib.pa_test_stall_next_launch({"decode": 0, "prefill": 1, "shared_prefix": 3}[kernel], int(cta)),
            "pa_test_stall_next_launch")
 
 

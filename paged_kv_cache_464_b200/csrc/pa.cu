@@ -1,8 +1,7 @@
 // pa.cu -- the C ABI of libpa_b200.so (declared in include/pa.h): host-side
 // argument checks, TMA descriptor encoding and kernel launches.  The kernels
-// themselves live in pa_cache_ops.cuh, pa_decode.cuh and pa_prefill.cuh, compiled here as one
-// translation unit so that the per-device error word needs no separate
-// device linking.
+// themselves live in the pa_*.cuh headers, compiled here as one translation
+// unit so that the per-device error word needs no separate device linking.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -19,6 +18,9 @@
 #include "pa_prefill.cuh"
 #include "pa_decode_fp8tc.cuh"
 #include "pa_probe.cuh"
+#include "pa_rope.cuh"
+#include "pa_shared_prefix.cuh"
+#include "pa_sparse.cuh"
 
 #ifndef PA_PROGRAMMATIC_LAUNCH
 #define PA_PROGRAMMATIC_LAUNCH 1
@@ -60,6 +62,7 @@ int sm_count() {
 // decode or prefill launch of the armed kind; 0 = not armed.
 std::atomic<int> g_stall_decode{0};
 std::atomic<int> g_stall_prefill{0};
+std::atomic<int> g_stall_prefix{0};
 
 int elem_bytes(pa_dtype_t dt) {
   switch (dt) {
@@ -654,6 +657,566 @@ pa_status_t pa_decode_static_workspace(void *out, const void *q, const void *k_c
   return launch_planned(d, scratch, stream);
 }
 
+// ---------------------------------------------------------------- rotate and append
+pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, double base, void *stream) {
+  if (max_position <= 0 || rotary_dim <= 0 || rotary_dim % 2 != 0 || !std::isfinite(base) || base <= 0.0)
+    return PA_ERR_SHAPE;
+  if (!cos_sin) return PA_ERR_NULL;
+  if (!aligned(cos_sin, 16)) return PA_ERR_ALIGN;
+  const long long total = (long long)max_position * (rotary_dim / 2);
+  long long ctas = (total + 255) / 256;
+  if (ctas > 32LL * sm_count()) ctas = 32LL * sm_count();
+  return launch(pa::rope_table_kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, cos_sin, max_position,
+                rotary_dim / 2, base);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Do the byte ranges of two sets of rows (first address, rows, stride, row bytes) overlap?
+bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+template <typename T>
+pa_status_t launch_rope(const pa::RopeParams &p, bool interleaved, bool fp8, cudaStream_t stream) {
+  const int H = p.num_heads + 2 * p.num_kv_heads;
+  const int HS = (H + p.heads_per_thread - 1) / p.heads_per_thread;
+  const long long total = (long long)p.num_tokens * HS * (pa::kChunksPerRow / 2);
+  long long ctas = (total + 255) / 256;
+  if (ctas > 64LL * sm_count()) ctas = 64LL * sm_count();
+  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)ctas), dim3(256), 0, stream, p); };
+  if constexpr (!std::is_same<T, float>::value) {
+    if (fp8)
+      return interleaved ? go(pa::rope_and_cache_kernel<T, true, true>) : go(pa::rope_and_cache_kernel<T, false, true>);
+  }
+  return interleaved ? go(pa::rope_and_cache_kernel<T, true, false>) : go(pa::rope_and_cache_kernel<T, false, false>);
+}
+
+// cache_dtype: dtype, or PA_FP8_E4M3.
+pa_status_t rope_impl(void *q_out, const void *q, const void *key, const void *value, void *k_cache, void *v_cache,
+                      const int64_t *positions, const float *cos_sin, const int64_t *slot_mapping, int num_tokens,
+                      int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride, int max_position,
+                      int rotary_dim, int interleaved, int64_t num_blocks, int block_size, int num_heads,
+                      int num_kv_heads, int head_dim, pa_dtype_t dtype, pa_dtype_t cache_dtype, float k_scale,
+                      float v_scale, void *stream) {
+  pa_status_t st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim, cache_dtype);
+  if (st != PA_OK) return st;
+  const int es = elem_bytes(dtype), epc = 16 / es;
+  if (num_tokens < 0 || num_heads <= 0 || num_heads > 65536 || num_kv_heads > 65536 || max_position <= 0 ||
+      rotary_dim <= 0 || rotary_dim > head_dim || rotary_dim % (2 * epc) != 0)
+    return PA_ERR_SHAPE;
+  if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f) return PA_ERR_SHAPE;
+  const int64_t q_row = (int64_t)num_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride > INT32_MAX ||
+      q_out_stride > INT32_MAX || k_stride > INT32_MAX || v_stride > INT32_MAX)
+    return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !key || !value || !k_cache || !v_cache || !positions || !cos_sin || !slot_mapping)
+    return PA_ERR_NULL;
+  if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(positions, 8) || !aligned(slot_mapping, 8) ||
+      q_stride % epc != 0 || q_out_stride % epc != 0 || k_stride % epc != 0 || v_stride % epc != 0)
+    return PA_ERR_ALIGN;
+  auto span = [&](int64_t stride, int64_t row) { return (size_t)((num_tokens - 1) * stride + row) * es; };
+  if (!(q_out == q && q_out_stride == q_stride) &&
+      (ranges_overlap(q_out, span(q_out_stride, q_row), q, span(q_stride, q_row)) ||
+       ranges_overlap(q_out, span(q_out_stride, q_row), key, span(k_stride, kv_row)) ||
+       ranges_overlap(q_out, span(q_out_stride, q_row), value, span(v_stride, kv_row))))
+    return PA_ERR_SHAPE;
+  pa::RopeParams p{};
+  p.q_out = q_out;
+  p.q = q;
+  p.key = key;
+  p.value = value;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slot_mapping = slot_mapping;
+  p.q_out_stride = q_out_stride;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.num_slots = num_blocks * block_size;
+  p.max_position = max_position;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rotary = rotary_dim;
+  p.heads_per_thread = 1;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  const bool fp8 = cache_dtype == PA_FP8_E4M3;
+  cudaStream_t s = (cudaStream_t)stream;
+  switch (dtype) {
+    case PA_F32: return launch_rope<float>(p, interleaved != 0, fp8, s);
+    case PA_F16: return launch_rope<__half>(p, interleaved != 0, fp8, s);
+    case PA_BF16: return launch_rope<__nv_bfloat16>(p, interleaved != 0, fp8, s);
+    case PA_FP8_E4M3: break;
+  }
+  return PA_ERR_DTYPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status_t pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                              void *v_cache, const int64_t *positions, const float *cos_sin,
+                              const int64_t *slot_mapping, int num_tokens, int64_t q_out_stride, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int max_position, int rotary_dim, int interleaved,
+                              int64_t num_blocks, int block_size, int num_heads, int num_kv_heads, int head_dim,
+                              pa_dtype_t dtype, void *stream) {
+  if (dtype == PA_FP8_E4M3) return PA_ERR_DTYPE;   // pa_rope_and_cache_fp8
+  return rope_impl(q_out, q, key, value, k_cache, v_cache, positions, cos_sin, slot_mapping, num_tokens, q_out_stride,
+                   q_stride, k_stride, v_stride, max_position, rotary_dim, interleaved, num_blocks, block_size,
+                   num_heads, num_kv_heads, head_dim, dtype, dtype, 1.f, 1.f, stream);
+}
+
+pa_status_t pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                                  void *v_cache, const int64_t *positions, const float *cos_sin,
+                                  const int64_t *slot_mapping, int num_tokens, int64_t q_out_stride, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, int max_position, int rotary_dim,
+                                  int interleaved, int64_t num_blocks, int block_size, int num_heads,
+                                  int num_kv_heads, int head_dim, pa_dtype_t src_dtype, float k_scale, float v_scale,
+                                  void *stream) {
+  if (src_dtype != PA_F16 && src_dtype != PA_BF16) return PA_ERR_DTYPE;
+  return rope_impl(q_out, q, key, value, k_cache, v_cache, positions, cos_sin, slot_mapping, num_tokens, q_out_stride,
+                   q_stride, k_stride, v_stride, max_position, rotary_dim, interleaved, num_blocks, block_size,
+                   num_heads, num_kv_heads, head_dim, src_dtype, PA_FP8_E4M3, k_scale, v_scale, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- shared prefix
+namespace {
+
+// How pa_decode_shared_prefix cuts its work: partitions of the prefix, and the
+// suffix's split-K; the workspace has `slots` partials a row, the suffix's from slot0 on.
+struct PrefixPlan {
+  int row_ctas, parts, part_tokens, suffix_partition, suffix_parts, slot0, slots;
+  WorkspaceLayout ws;
+};
+
+// Partitions: as many as give the shortest run, a wave of one CTA an SM taking
+// the tiles of its longest partition plus about three tiles' time of set-up and epilogue.
+PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_prefix_len,
+                       int max_suffix_len, int max_group_size) {
+  PrefixPlan r{};
+  const int group = num_heads / num_kv_heads;
+  const int rows = max_group_size * group;
+  r.row_ctas = (rows + 2 * pa::kPrefixRows - 1) / (2 * pa::kPrefixRows);
+  const int tiles = (max_prefix_len + pa::kPrefixKv - 1) / pa::kPrefixKv;
+  if (tiles > 0) {
+    const long long ctas = (long long)num_groups * r.row_ctas * num_kv_heads;
+    const int sms = sm_count();
+    long long best = INT64_MAX;
+    int per = tiles;
+    for (int parts = 1; parts <= tiles && parts <= 64; ++parts) {
+      const int t = (tiles + parts - 1) / parts;
+      const long long waves = (ctas * parts + sms - 1) / sms;
+      const long long cost = waves * (t + 3);
+      if (cost < best) {
+        best = cost;
+        per = t;
+      }
+    }
+    r.part_tokens = per * pa::kPrefixKv;
+    r.parts = (tiles + per - 1) / per;
+  }
+  r.suffix_partition = resolve_partition_size(num_seqs, num_heads, num_kv_heads, head_dim, max_suffix_len, 0);
+  r.suffix_parts = max_partitions(max_suffix_len, r.suffix_partition);
+  r.slot0 = 2 * r.parts;
+  r.slots = r.slot0 + r.suffix_parts;
+  const size_t n = (size_t)num_seqs * num_heads * r.slots;
+  r.ws.l_off = align256(n * sizeof(float));
+  r.ws.o_off = 2 * r.ws.l_off;
+  r.ws.bytes = r.ws.o_off + align256(n * head_dim * sizeof(float));
+  return r;
+}
+
+pa_status_t prefix_shape_status(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int max_prefix_len,
+                                int max_suffix_len, int max_group_size) {
+  if (num_seqs < 0 || num_groups < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      max_prefix_len < 0 || max_prefix_len % kBlockSize != 0 || max_suffix_len < 0 || max_group_size < 0 ||
+      max_prefix_len > (1 << 30) || max_suffix_len > (1 << 30) || max_group_size > (1 << 24))
+    return PA_ERR_SHAPE;
+  const int group = num_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_SHAPE;
+  if (num_seqs > 0 && (num_groups == 0 || max_group_size == 0)) return PA_ERR_SHAPE;
+  return PA_OK;
+}
+
+template <typename T, int G, typename Math>
+pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa::PrefixParams &p, int num_groups,
+                          cudaStream_t stream) {
+  pa_status_t st;
+  if (p.parts > 0) {
+    auto kernel = pa::pa_shared_prefix_kernel<T, G>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::PrefixSmem::kAlloc) != cudaSuccess)
+      return PA_ERR_CUDA;
+    const long long grid = (long long)num_groups * p.row_ctas * p.num_kv_heads * p.parts;
+    if (grid > INT32_MAX) return PA_ERR_SHAPE;
+    st = launch(kernel, dim3((unsigned)grid), dim3(pa::kPrefixThreads), pa::PrefixSmem::kAlloc, stream, mk, mv, p);
+    if (st != PA_OK) return st;
+  }
+  using SM = pa::DecodeSmem<T, G, Math>;
+  auto suffix = pa::pa_decode_partition_kernel<T, G, Math, pa::kDecodeWarps, pa::kWalkSuffix>;
+  if (cudaFuncSetAttribute(suffix, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.max_partitions;
+  if (grid > INT32_MAX) return PA_ERR_SHAPE;
+  pa::SuffixParams sp = p;
+  sp.stall_cta = 0;
+  st = launch(suffix, dim3((unsigned)grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, sp);
+  if (st != PA_OK) return st;
+  const long long rows = (long long)p.num_seqs * p.num_heads;
+  long long ctas = (rows + pa::kReduceWarps - 1) / pa::kReduceWarps;
+  if (ctas > 8LL * sm_count()) ctas = 8LL * sm_count();
+  return launch(pa::pa_join_shared_kernel<T, G>, dim3((unsigned)ctas), dim3(pa::kReduceWarps * 32), 0, stream, p);
+}
+
+template <typename T>
+pa_status_t dispatch_prefix(int group, const CUtensorMap &mk, const CUtensorMap &mv, const pa::PrefixParams &p,
+                            int num_groups, cudaStream_t s) {
+  switch (group) {
+    case 1: return launch_prefix<T, 1, pa::FmaMath<T, 1>>(mk, mv, p, num_groups, s);
+    case 2: return launch_prefix<T, 2, pa::MmaMath<T, 2>>(mk, mv, p, num_groups, s);
+    case 4: return launch_prefix<T, 4, pa::MmaMath<T, 4>>(mk, mv, p, num_groups, s);
+    case 8: return launch_prefix<T, 8, pa::MmaMath<T, 8>>(mk, mv, p, num_groups, s);
+  }
+  return PA_ERR_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_heads, int num_kv_heads,
+                                               int head_dim, int max_prefix_len, int max_suffix_len,
+                                               int max_group_size) {
+  if (prefix_shape_status(num_seqs, num_groups, num_heads, num_kv_heads, max_prefix_len, max_suffix_len,
+                          max_group_size) != PA_OK ||
+      head_dim != 128 || num_seqs == 0)
+    return 0;
+  return plan_prefix(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len, max_suffix_len,
+                     max_group_size).ws.bytes;
+}
+
+pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                    const int32_t *group_start, const int32_t *prefix_lens, int num_seqs,
+                                    int num_groups, int num_heads, int max_prefix_len, int max_suffix_len,
+                                    int max_group_size, float scale, void *workspace, size_t workspace_bytes,
+                                    int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                    pa_dtype_t dtype, void *stream) {
+  pa_status_t st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_DTYPE;
+  st = prefix_shape_status(num_seqs, num_groups, num_heads, num_kv_heads, max_prefix_len, max_suffix_len, max_group_size);
+  if (st != PA_OK) return st;
+  if (max_blocks_per_seq < 0 || (long long)max_blocks_per_seq * kBlockSize > INT32_MAX || !std::isfinite(scale) ||
+      !(scale > 0.f))
+    return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !context_lens || !group_start || !prefix_lens ||
+      (max_blocks_per_seq > 0 && !block_tables))
+    return PA_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(group_start, 4) || !aligned(prefix_lens, 4))
+    return PA_ERR_ALIGN;
+  const PrefixPlan plan = plan_prefix(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len,
+                                      max_suffix_len, max_group_size);
+  if (!workspace || workspace_bytes < plan.ws.bytes) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  CUtensorMap mk, mv;
+  if (!encode_cache_map(&mk, k_cache, num_blocks, num_kv_heads, kRowBytes) ||
+      !encode_cache_map(&mv, v_cache, num_blocks, num_kv_heads, kRowBytes))
+    return PA_ERR_CUDA;
+  char *w = static_cast<char *>(workspace);
+  pa::PrefixParams p{};
+  p.out = out;
+  p.q = q;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.ws_m = reinterpret_cast<float *>(w);
+  p.ws_l = reinterpret_cast<float *>(w + plan.ws.l_off);
+  p.ws_o = reinterpret_cast<float *>(w + plan.ws.o_off);
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_context_len = max_suffix_len;
+  p.partition_size = plan.suffix_partition;
+  p.max_partitions = plan.suffix_parts;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.v_scale = 1.f;
+  p.stall_cta = g_stall_prefix.exchange(0);
+  p.group_start = group_start;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  p.max_prefix_len = max_prefix_len;
+  p.max_group_size = max_group_size;
+  p.slots = plan.slots;
+  p.slot0 = plan.slot0;
+  p.parts = plan.parts;
+  p.part_tokens = plan.part_tokens > 0 ? plan.part_tokens : pa::kPrefixKv;
+  p.row_ctas = plan.row_ctas;
+  const int group = num_heads / num_kv_heads;
+  cudaStream_t s = (cudaStream_t)stream;
+  return dtype == PA_F16 ? dispatch_prefix<__half>(group, mk, mv, p, num_groups, s)
+                         : dispatch_prefix<__nv_bfloat16>(group, mk, mv, p, num_groups, s);
+}
+
+// ---------------------------------------------------------------- block-sparse decode
+pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *context_lens, const int32_t *new_lens,
+                                   int num_seqs, int max_new_len, int64_t num_blocks, int block_size,
+                                   int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream) {
+  if (dtype == PA_FP8_E4M3) return PA_ERR_DTYPE;
+  pa_status_t st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_new_len < 0 || max_blocks_per_seq < 0 || num_kv_heads > 65536 ||
+      (long long)max_blocks_per_seq * kBlockSize > INT32_MAX)
+    return PA_ERR_SHAPE;
+  if (num_seqs == 0 || max_new_len == 0) return PA_OK;
+  if (!k_cache || !block_bounds || !context_lens || !new_lens || (max_blocks_per_seq > 0 && !block_tables))
+    return PA_ERR_NULL;
+  if (!aligned(k_cache, 16) || !aligned(block_bounds, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+      !aligned(new_lens, 4))
+    return PA_ERR_ALIGN;
+  pa::BoundsParams p{};
+  p.k_cache = (const uint4 *)k_cache;
+  p.bounds = (uint4 *)block_bounds;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.new_lens = new_lens;
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.chunks_per_token = num_kv_heads * pa::kChunksPerRow;
+  p.max_new_len = max_new_len;
+  // the new tokens may start anywhere in a block: n tokens touch at most ceil((n + 15) / 16) blocks
+  p.blocks_per_seq = (int)(((long long)max_new_len + 2 * kBlockSize - 2) / kBlockSize);
+  const long long total = (long long)num_seqs * p.blocks_per_seq * p.chunks_per_token;
+  long long ctas = (total + 127) / 128;
+  if (ctas > 64LL * sm_count()) ctas = 64LL * sm_count();
+  cudaStream_t s = (cudaStream_t)stream;
+  switch (dtype) {
+    case PA_F32: return launch(pa::block_bounds_kernel<float>, dim3((unsigned)ctas), dim3(128), 0, s, p);
+    case PA_F16: return launch(pa::block_bounds_kernel<__half>, dim3((unsigned)ctas), dim3(128), 0, s, p);
+    case PA_BF16: return launch(pa::block_bounds_kernel<__nv_bfloat16>, dim3((unsigned)ctas), dim3(128), 0, s, p);
+    case PA_FP8_E4M3: break;
+  }
+  return PA_ERR_DTYPE;
+}
+
+}  // extern "C"
+
+namespace {
+
+template <typename T>
+pa_status_t launch_scores(int group, const pa::SelectParams &p, cudaStream_t s) {
+  const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.chunks;
+  if (grid > INT32_MAX) return PA_ERR_SHAPE;
+  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)grid), dim3(pa::kScoreWarps * 32), 0, s, p); };
+  switch (group) {
+    case 1: return go(pa::block_score_kernel<T, 1>);
+    case 2: return go(pa::block_score_kernel<T, 2>);
+    case 4: return go(pa::block_score_kernel<T, 4>);
+    case 8: return go(pa::block_score_kernel<T, 8>);
+  }
+  return PA_ERR_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len <= 0) return 0;
+  const size_t blocks = ((size_t)max_context_len + kBlockSize - 1) / kBlockSize;
+  return align256((size_t)num_seqs * num_kv_heads * blocks * sizeof(unsigned long long));
+}
+
+pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block_bounds, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_heads,
+                             int max_context_len, int num_selected, int sink_blocks, int recent_blocks,
+                             void *workspace, size_t workspace_bytes, int64_t num_blocks, int block_size,
+                             int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream) {
+  if (dtype == PA_FP8_E4M3) return PA_ERR_DTYPE;
+  pa_status_t st = cache_shape_status(num_blocks, block_size, num_kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_heads <= 0 || num_heads % num_kv_heads != 0 || max_context_len < 0 ||
+      max_blocks_per_seq < 0 || (long long)max_blocks_per_seq * kBlockSize > INT32_MAX || num_selected <= 0 ||
+      sink_blocks < 0 || recent_blocks < 0 || (long long)sink_blocks + recent_blocks > num_selected ||
+      num_selected > (1 << 27))
+    return PA_ERR_SHAPE;
+  const int group = num_heads / num_kv_heads;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_SHAPE;
+  if ((long long)num_seqs * num_kv_heads > INT32_MAX) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!selected || !q || !block_bounds || !context_lens || (max_blocks_per_seq > 0 && !block_tables)) return PA_ERR_NULL;
+  if (!aligned(selected, 4) || !aligned(q, 16) || !aligned(block_bounds, 16) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4))
+    return PA_ERR_ALIGN;
+  const size_t need = pa_select_blocks_workspace_bytes(num_seqs, num_kv_heads, max_context_len);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  }
+  pa::SelectParams p{};
+  p.q = q;
+  p.bounds = (const uint4 *)block_bounds;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.keys = (unsigned long long *)workspace;
+  p.selected = selected;
+  p.num_blocks = num_blocks;
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_context_len = max_context_len;
+  p.max_blocks = (int)(((long long)max_context_len + kBlockSize - 1) / kBlockSize);
+  p.num_selected = num_selected;
+  p.sink = sink_blocks;
+  p.recent = recent_blocks;
+  p.chunks = (p.max_blocks + pa::kScoreBlocks - 1) / pa::kScoreBlocks;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (p.max_blocks > num_selected) {   // else no sequence has more blocks than are chosen
+    switch (dtype) {
+      case PA_F32: st = launch_scores<float>(group, p, s); break;
+      case PA_F16: st = launch_scores<__half>(group, p, s); break;
+      case PA_BF16: st = launch_scores<__nv_bfloat16>(group, p, s); break;
+      case PA_FP8_E4M3: return PA_ERR_DTYPE;
+    }
+    if (st != PA_OK) return st;
+  }
+  return launch(pa::block_select_kernel, dim3((unsigned)(num_seqs * num_kv_heads)), dim3(pa::kSelectThreads), 0, s, p);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Blocks a partition of a selected-block decode: enough CTAs for two waves of
+// three an SM, from 4 blocks (one a warp) to 64.
+int selected_partition(int num_seqs, int num_kv_heads, int num_selected) {
+  const long long want = 6LL * sm_count();
+  const long long pairs = (long long)num_seqs * num_kv_heads;
+  long long parts = (want + pairs - 1) / pairs;
+  long long blocks = (num_selected + parts - 1) / parts;
+  if (blocks < 4) blocks = 4;
+  if (blocks > 64) blocks = 64;
+  return (int)(blocks + 3) / 4 * 4 * kBlockSize;
+}
+
+template <typename T, int G, typename Math>
+pa_status_t launch_selected(const CUtensorMap &mk, const CUtensorMap &mv, const pa::SelectedParams &p,
+                            cudaStream_t stream) {
+  using SM = pa::DecodeSmem<T, G, Math>;
+  auto kernel = pa::pa_decode_partition_kernel<T, G, Math, pa::kDecodeWarps, pa::kWalkSelected>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.max_partitions;
+  if (grid > INT32_MAX) return PA_ERR_SHAPE;
+  const pa_status_t st =
+      launch(kernel, dim3((unsigned)grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, p);
+  if (st != PA_OK || p.max_partitions <= 1) return st;
+  const long long rows = (long long)p.num_seqs * p.num_heads;
+  long long ctas = (rows + pa::kReduceWarps - 1) / pa::kReduceWarps;
+  if (ctas > 8LL * sm_count()) ctas = 8LL * sm_count();
+  return launch(pa::pa_join_selected_kernel<T>, dim3((unsigned)ctas), dim3(pa::kReduceWarps * 32), 0, stream, p);
+}
+
+template <typename T>
+pa_status_t dispatch_selected(int group, const CUtensorMap &mk, const CUtensorMap &mv, const pa::SelectedParams &p,
+                              cudaStream_t s) {
+  constexpr bool kMma = !std::is_same<T, float>::value;
+  switch (group) {
+    case 1: return launch_selected<T, 1, pa::FmaMath<T, 1>>(mk, mv, p, s);
+    case 2:
+      if constexpr (kMma) return launch_selected<T, 2, pa::MmaMath<T, 2>>(mk, mv, p, s);
+      else return launch_selected<T, 2, pa::FmaMath<T, 2>>(mk, mv, p, s);
+    case 4:
+      if constexpr (kMma) return launch_selected<T, 4, pa::MmaMath<T, 4>>(mk, mv, p, s);
+      else return launch_selected<T, 4, pa::FmaMath<T, 4>>(mk, mv, p, s);
+    case 8:
+      if constexpr (kMma) return launch_selected<T, 8, pa::MmaMath<T, 8>>(mk, mv, p, s);
+      else return launch_selected<T, 8, pa::FmaMath<T, 8>>(mk, mv, p, s);
+  }
+  return PA_ERR_SHAPE;
+}
+
+WorkspaceLayout selected_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int num_selected) {
+  const int blocks = selected_partition(num_seqs, num_kv_heads, num_selected) / kBlockSize;
+  return workspace_layout(num_seqs, num_heads, num_kv_heads, head_dim, (num_selected + blocks - 1) / blocks);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pa_decode_selected_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                          int num_selected) {
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_selected <= 0 ||
+      num_selected > (1 << 27))
+    return 0;
+  return selected_workspace(num_seqs, num_heads, num_kv_heads, head_dim, num_selected).bytes;
+}
+
+pa_status_t pa_decode_selected(void *out, const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                               const int32_t *selected, int num_seqs, int num_heads, int num_selected, float scale,
+                               void *workspace, size_t workspace_bytes, int64_t num_blocks, int block_size,
+                               int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream) {
+  if (dtype == PA_FP8_E4M3) return PA_ERR_DTYPE;
+  if (num_selected <= 0 || num_selected > (1 << 27)) return PA_ERR_SHAPE;
+  if (num_seqs > 0 && !selected) return PA_ERR_NULL;
+  if (!aligned(selected, 4)) return PA_ERR_ALIGN;
+  // every other check is pa_decode's (one partition: the split is planned below)
+  const long long capacity = (long long)max_blocks_per_seq * kBlockSize;
+  DecodePlan d;
+  const pa_status_t st = plan_decode(d, out, q, nullptr, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                     context_lens, num_seqs, num_heads,
+                                     capacity < 0 || capacity > INT32_MAX ? 0 : (int)capacity, scale, 0, num_blocks,
+                                     block_size, num_kv_heads, head_dim, dtype, dtype, 1.f, 1.f);
+  if (st != PA_OK || d.empty) return st;
+  const WorkspaceLayout ws = selected_workspace(num_seqs, num_heads, num_kv_heads, head_dim, num_selected);
+  if (ws.bytes > 0) {
+    if (!workspace || workspace_bytes < ws.bytes) return PA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  }
+  if (!encode_cache_map(&d.mk, k_cache, num_blocks, num_kv_heads, kRowBytes) ||
+      !encode_cache_map(&d.mv, v_cache, num_blocks, num_kv_heads, kRowBytes))
+    return PA_ERR_CUDA;
+  pa::SelectedParams p{};
+  static_cast<pa::DecodeParams &>(p) = d.p;
+  char *w = static_cast<char *>(workspace);
+  if (ws.bytes > 0) {
+    p.ws_m = reinterpret_cast<float *>(w + ws.m_off);
+    p.ws_l = reinterpret_cast<float *>(w + ws.l_off);
+    p.ws_o = reinterpret_cast<float *>(w + ws.o_off);
+  }
+  p.partition_size = selected_partition(num_seqs, num_kv_heads, num_selected);
+  p.max_partitions = (num_selected + p.partition_size / kBlockSize - 1) / (p.partition_size / kBlockSize);
+  p.selected = selected;
+  p.num_selected = num_selected;
+  cudaStream_t s = (cudaStream_t)stream;
+  switch (dtype) {
+    case PA_F32: return dispatch_selected<float>(d.group, d.mk, d.mv, p, s);
+    case PA_F16: return dispatch_selected<__half>(d.group, d.mk, d.mv, p, s);
+    case PA_BF16: return dispatch_selected<__nv_bfloat16>(d.group, d.mk, d.mv, p, s);
+    case PA_FP8_E4M3: break;
+  }
+  return PA_ERR_DTYPE;
+}
+
 pa_status_t pa_stream_read(const void *buf, size_t bytes, uint64_t *sink, void *stream) {
   if (bytes % 16 != 0) return PA_ERR_SHAPE;
   if (bytes == 0) return PA_OK;
@@ -673,6 +1236,7 @@ pa_status_t pa_test_stall_next_launch(int kernel, int64_t cta) {
   switch (kernel) {
     case 0: g_stall_decode.store(armed); return PA_OK;
     case 1: g_stall_prefill.store(armed); return PA_OK;
+    case 3: g_stall_prefix.store(armed); return PA_OK;
   }
   return PA_ERR_SHAPE;
 }

@@ -94,6 +94,69 @@ struct DecodeParams {
   int stall_cta;                  // test hook (pa_common.cuh): 0 in every ordinary launch
 };
 
+// Which tokens of a sequence a partition launch walks (the kernel's kWalk):
+//   kWalkAll       tokens 0 .. L-1 (pa_decode, pa_decode_append, pa_decode_fp8)
+//   kWalkSuffix    the tokens after the sequence's shared prefix
+//                  (pa_decode_shared_prefix; the prefix's partials come from
+//                  pa_shared_prefix.cuh).  Every partition leaves a partial.
+//   kWalkSelected  the tokens of the blocks that a list names, one list for each
+//                  (sequence, KV head) (pa_decode_selected)
+constexpr int kWalkAll = 0, kWalkSuffix = 1, kWalkSelected = 2;
+
+struct SuffixParams : DecodeParams {   // context_lens: whole lengths; max_context_len: of the suffix
+  const int32_t *group_start;     // [num_groups + 1]
+  const int32_t *prefix_lens;     // [num_groups]
+  int num_groups, max_prefix_len, max_group_size;
+  int slots, slot0;               // partials of a row in the workspace; the first of the suffix's
+};
+
+struct SelectedParams : DecodeParams {
+  const int32_t *selected;        // [S][Hkv][num_selected] logical blocks; < 0: no block
+  int num_selected;
+};
+
+template <int kWalk>
+struct WalkParams {
+  using type = DecodeParams;
+};
+template <>
+struct WalkParams<kWalkSuffix> {
+  using type = SuffixParams;
+};
+template <>
+struct WalkParams<kWalkSelected> {
+  using type = SelectedParams;
+};
+
+// The group that sequence b is in (sequences group_start[i] .. group_start[i+1]-1
+// are group i) and its prefix; called by whole warps, every lane with the same b.
+// ok = false if the group's entries are out of range (nothing is read with them).
+struct PrefixGroup {
+  int index, s0, s1, prefix;
+  bool ok;
+};
+
+__device__ __forceinline__ PrefixGroup group_of(const SuffixParams &p, int b) {
+  int n = 0;   // groups that start at or before b
+  for (int i0 = 0; i0 < p.num_groups; i0 += 32) {
+    const int i = i0 + (threadIdx.x & 31);
+    n += __popc(__ballot_sync(kFullMask, i < p.num_groups && p.group_start[i] <= b));
+  }
+  PrefixGroup r;
+  r.index = n - 1;
+  r.ok = n > 0;
+  r.s0 = r.s1 = r.prefix = 0;
+  if (r.ok) {
+    r.s0 = p.group_start[r.index];
+    r.s1 = p.group_start[r.index + 1];
+    r.prefix = p.prefix_lens[r.index];
+    r.ok = r.s0 >= 0 && r.s0 <= b && b < r.s1 && r.s1 <= p.num_seqs && r.s1 - r.s0 <= p.max_group_size &&
+           r.prefix >= 0 && r.prefix <= p.max_prefix_len && r.prefix % kBlockSize == 0 &&
+           r.prefix / kBlockSize <= p.max_blocks_per_seq;
+  }
+  return r;
+}
+
 // Byte offset of 16-byte chunk `c` (0..15) of token `t` in a swizzled tile.
 __device__ __forceinline__ int tile_offset(int t, int c) {
   return ((c >> 3) * kBlockSize + t) * 128 + (((c & 7) ^ (t & 7)) << 4);
@@ -730,10 +793,10 @@ __global__ void __launch_bounds__(256) zero_counts_kernel(unsigned *count, int n
 // default launch shape), or six of the two-warp shape.
 constexpr int decode_min_ctas(int warps) { return warps == 2 ? 6 : PA_DECODE_MIN_CTAS_PER_SM; }
 
-template <typename T, int G, typename Math, int W = kDecodeWarps>
+template <typename T, int G, typename Math, int W = kDecodeWarps, int kWalk = kWalkAll>
 __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     pa_decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                               const DecodeParams p) {
+                               const typename WalkParams<kWalk>::type p) {
   static_assert(!Math::kNeedsQInSmem || W == kDecodeWarps, "the CUDA-core block math stages q with kDecodeWarps warps");
   using SM = DecodeSmem<T, G, Math, W>;
   constexpr int D = SM::D;
@@ -763,24 +826,40 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
   item /= p.max_partitions;
   const int g = item % p.num_kv_heads;
   const int b = item / p.num_kv_heads;
-  const int L = p.context_lens[b];
+  int L = p.context_lens[b];
+  int block0 = 0;   // first logical block walked
+  if constexpr (kWalk == kWalkSuffix) {
+    const PrefixGroup group = group_of(p, b);
+    if (!group.ok) {
+      if (part == 0 && g == 0 && threadIdx.x == 0) record_error(8 /*PA_DEV_BAD_GROUP*/, group.index);
+      return;
+    }
+    if (L < group.prefix || L > p.max_blocks_per_seq * kBlockSize) L = -1;
+    else L -= group.prefix;
+    block0 = group.prefix / kBlockSize;
+  }
   if (L < 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize) {
     if (part == 0 && g == 0 && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
     return;
   }
   const int P = p.partition_size;
-  const int nparts = (L + P - 1) / P;
+  const int nparts = kWalk == kWalkSelected ? p.max_partitions : (L + P - 1) / P;
   const int h0 = g * G;   // first query head of this KV head (contiguous groups)
   T *out = reinterpret_cast<T *>(p.out) + (static_cast<size_t>(b) * p.num_heads + h0) * D;
   if (L == 0) {   // empty context: the row is the empty sum, zeros
-    if (part == 0)
+    if (part == 0 && kWalk != kWalkSuffix)
       for (int i = threadIdx.x * 4; i < G * D; i += (W * 32) * 4) Elem<T>::store4(out + i, 0.f, 0.f, 0.f, 0.f);
     return;
   }
   if (part >= nparts) return;
   const int tok0 = part * P;
   const int tok1 = min(tok0 + P, L);
-  const int nblk = (tok1 - tok0 + kBlockSize - 1) / kBlockSize;
+  int nblk = (tok1 - tok0 + kBlockSize - 1) / kBlockSize;
+  const int32_t *sel_row = nullptr;   // this partition's entries of the list
+  if constexpr (kWalk == kWalkSelected) {
+    nblk = min(P / kBlockSize, p.num_selected - part * (P / kBlockSize));
+    sel_row = p.selected + (static_cast<size_t>(b) * p.num_kv_heads + g) * p.num_selected + part * (P / kBlockSize);
+  }
   const T *qg = reinterpret_cast<const T *>(p.q) + (static_cast<size_t>(b) * p.num_heads + h0) * D;
 
   if (threadIdx.x == 0) {
@@ -793,9 +872,12 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
 
   // ---- this warp's blocks: local block index warp + j * W, j = 0 .. nw-1
   const int nw = nblk > warp ? (nblk - warp + W - 1) / W : 0;
-  const int32_t *bt_row = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + tok0 / kBlockSize;
+  const int32_t *bt_row = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + block0 +
+                          (kWalk == kWalkSelected ? 0 : tok0 / kBlockSize);
   int id_group = -1;   // which 32 consecutive j's the lanes' ids belong to
   int my_id = -1;      // lane l holds the physical id of j = 32 * id_group + l
+  int my_valid = 0;    // kWalkSelected: and how many of its tokens count (0 = no block)
+  uint32_t stage_valid = 0;   // kWalkSelected: the counts of the blocks in flight, 8 bits a stage
   const uint64_t policy = policy_evict_first();
 
   auto issue = [&](int j) {   // called by all 32 lanes, j warp-uniform
@@ -803,7 +885,20 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       id_group = j >> 5;
       const int jj = (id_group << 5) + lane;
       my_id = -1;
-      if (jj < nw) {
+      if constexpr (kWalk == kWalkSelected) {
+        my_valid = 0;
+        const int lb = jj < nw ? sel_row[warp + jj * W] : -1;
+        if (lb >= 0) {
+          // at or past the sequence's end: nothing of the block's counts
+          const int id = lb <= (L - 1) / kBlockSize ? bt_row[lb] : -1;
+          if (id < 0 || id >= p.num_blocks) {
+            record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, lb <= (L - 1) / kBlockSize ? id : lb);
+          } else {
+            my_id = id;
+            my_valid = min(kBlockSize, L - lb * kBlockSize);
+          }
+        }
+      } else if (jj < nw) {
         const int id = bt_row[warp + jj * W];
         if (id < 0 || id >= p.num_blocks) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
         else my_id = id;
@@ -811,6 +906,11 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     }
     const int id = __shfl_sync(kFullMask, my_id, j & 31);
     const int s = warp + (j % kSPW) * W;
+    if constexpr (kWalk == kWalkSelected) {
+      const int at = 8 * (j % kSPW);
+      stage_valid = (stage_valid & ~(0xffu << at)) |
+                    (static_cast<uint32_t>(__shfl_sync(kFullMask, my_valid, j & 31)) << at);
+    }
     if (lane == 0 && !(stall_here && warp == 0 && j == 0)) {   // (test hook: warp 0's first stage left unissued)
       if (id >= 0) {
         // one box per 128-byte part of the rows: the tile lands as [part][token][128 B]
@@ -850,8 +950,9 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     }
     uint8_t *tk = smem + s * 2 * kTile;
     const int lb = warp + j * W;   // local block index
-    const int nvalid = min(kBlockSize, tok1 - (tok0 + lb * kBlockSize));
-    if (Math::kRowBytes == 256 && p.new_k != nullptr && part == nparts - 1 && lb == nblk - 1) {
+    int nvalid = min(kBlockSize, tok1 - (tok0 + lb * kBlockSize));
+    if constexpr (kWalk == kWalkSelected) nvalid = (stage_valid >> (8 * (j % kSPW))) & 0xff;
+    if (kWalk == kWalkAll && Math::kRowBytes == 256 && p.new_k != nullptr && part == nparts - 1 && lb == nblk - 1) {
       // append mode: this block holds position L-1.  Store the new token's K/V
       // rows of head g in the cache and put them into the tile that just landed
       // (its copy of that row may predate the store).  Lanes 0-15 move the 16
@@ -871,7 +972,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       *reinterpret_cast<uint4 *>(tk + (is_v ? kTile : 0) + tile_offset(t_new, c)) = x;
       __syncwarp();
     }
-    math.block(tk, tk + kTile, nvalid, lane, p.scale_log2);
+    if (kWalk != kWalkSelected || nvalid > 0) math.block(tk, tk + kTile, nvalid, lane, p.scale_log2);
     __syncwarp();   // all lanes done with the stage
     if (j + kSPW < nw) {
       fence_proxy_async_smem();
@@ -902,6 +1003,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
+      if (kWalk == kWalkSelected && m_s[w * G + hh] == -INFINITY && l_s[w * G + hh] == 0.f) continue;   // no block
       const float f = ex2(m_s[w * G + hh] - M);   // 0 for a warp that saw no token
       lsum += f * l_s[w * G + hh];
       const float4 x = *reinterpret_cast<const float4 *>(o_s + (w * G + hh) * D + d);
@@ -910,11 +1012,13 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       a.z += f * x.z;
       a.w += f * x.w;
     }
-    if (nparts == 1) {
-      const float inv = 1.f / lsum;
+    if (kWalk != kWalkSuffix && nparts == 1) {
+      const float inv = kWalk == kWalkSelected && lsum == 0.f ? 0.f : 1.f / lsum;   // an empty list: zeros
       Elem<T>::store4(out + i, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     } else {
-      const size_t row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.max_partitions + part;
+      size_t row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.max_partitions + part;
+      if constexpr (kWalk == kWalkSuffix)
+        row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.slots + p.slot0 + part;
       *reinterpret_cast<float4 *>(p.ws_o + row * D + d) = a;
       if (d == 0) {
         p.ws_m[row] = M;
@@ -922,7 +1026,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       }
     }
   }
-  if (nparts == 1 || p.ws_count == nullptr) return;
+  if (kWalk != kWalkAll || nparts == 1 || p.ws_count == nullptr) return;
 
   // ---- split sequence: the last of its nparts CTAs (per KV head) combines the
   // partials.  Publish this CTA's partial, then take a ticket; no CTA waits for
@@ -1040,6 +1144,79 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_decode_reduce_kernel(con
         Elem<T>::store2(out, acc[0] * inv, acc[1] * inv);
       }
     }
+  }
+}
+
+// Combine the partials of the shared-prefix and selected-block walks: a warp per
+// (sequence, query head) row, the same sums as pa_decode_reduce_kernel.  A row has
+// `slots` partials in the workspace, of which two runs are used: the first na
+// and nb from slot0 on.  A partial with m = -inf and l = 0 holds no token and its o
+// is not used; a row without any token is zeros.
+template <typename T, typename Params>
+__device__ __forceinline__ void join_row(const Params &p, long long row, int slots, int na, int slot0, int nb) {
+  constexpr int D = kChunksPerRow * Elem<T>::kPerChunk;
+  constexpr int PER_LANE = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float *m = p.ws_m + row * slots;
+  const float *l = p.ws_l + row * slots;
+  const float *o = p.ws_o + row * slots * D + lane * PER_LANE;
+  const int n = na + nb;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, m[i < na ? i : slot0 + i - na]);
+  M = warp_max(M);
+  float lsum = 0.f;
+  float acc[PER_LANE];
+#pragma unroll
+  for (int e = 0; e < PER_LANE; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kReduceBatch) {
+    const int iu = i0 + lane % kReduceBatch;
+    const bool live = lane < kReduceBatch && iu < n;
+    const int su = iu < na ? iu : slot0 + iu - na;
+    const float m_u = live ? m[su] : -INFINITY;
+    const float l_u = live ? l[su] : 0.f;
+    float w[kReduceBatch], li[kReduceBatch], x[kReduceBatch][PER_LANE];
+#pragma unroll
+    for (int u = 0; u < kReduceBatch; ++u) {   // every load of the batch in flight
+      const int i = min(i0 + u, n - 1);
+      w[u] = __shfl_sync(kFullMask, m_u, u);
+      li[u] = __shfl_sync(kFullMask, l_u, u);
+      const float *src = o + static_cast<size_t>(i < na ? i : slot0 + i - na) * D;
+      if constexpr (PER_LANE == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        x[u][0] = v.x; x[u][1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReduceBatch; ++u) {
+      if (w[u] == -INFINITY && li[u] == 0.f) continue;   // past the end, or without a token: o may be anything
+      const float wk = ex2(w[u] - M);
+      lsum += wk * li[u];
+#pragma unroll
+      for (int e = 0; e < PER_LANE; ++e) acc[e] += wk * x[u][e];
+    }
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+  T *out = reinterpret_cast<T *>(p.out) + row * D + lane * PER_LANE;
+  if constexpr (PER_LANE == 4) {
+    Elem<T>::store4(out, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+  } else {
+    Elem<T>::store2(out, acc[0] * inv, acc[1] * inv);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kReduceWarps * 32) pa_join_selected_kernel(const SelectedParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const long long rows = static_cast<long long>(p.num_seqs) * p.num_heads;
+  const long long step = static_cast<long long>(gridDim.x) * kReduceWarps;
+  for (long long row = static_cast<long long>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5); row < rows; row += step) {
+    const int L = p.context_lens[row / p.num_heads];
+    if (L <= 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize) continue;   // as the partition kernel
+    join_row<T>(p, row, p.max_partitions, p.max_partitions, 0, 0);
   }
 }
 

@@ -1,0 +1,448 @@
+// pa_shared_prefix.cuh -- decode attention of a group of sequences to the prefix
+// they share, once for all of them, on the 5th-generation tensor cores.
+// Included only from pa.cu.
+//
+// Sequences s0 .. s1-1 of a group have the same first `prefix` tokens (the same
+// blocks in their tables).  Their rows -- (s1 - s0) sequences times the G query
+// heads of a KV head -- all meet the same K and V, so the products are those of
+// one matrix: S = Q K^T with a row for each (sequence, head), O = P V.  Each row
+// keeps its own running maximum m and sum l (base 2); a partition of the prefix
+// leaves (m, l, o) of every row in the workspace, and pa_join_shared_kernel
+// combines them with the partials of the sequences' own tokens
+// (pa_decode.cuh, kWalkSuffix).  Read once instead of (s1 - s0) times, the prefix
+// costs 4 flops per row, token and head_dim element against 512 bytes a token.
+//
+// One CTA: a KV head, a partition of the prefix, up to 256 rows.  Two softmax
+// warpgroups w = 0, 1 (thread = row) each own a 128-row tile of S and O in tensor
+// memory (256 columns each).  With more than 128 rows ("pair"), they hold
+// different rows and share every K/V tile; with at most 128 ("split"), they
+// hold the same rows, tile w of every two, and leave a partial each.  K/V tiles are 128
+// tokens (eight blocks), 32 KiB: a product is M=128 N=128 K=16 throughout, the
+// widest form whose S (128 columns) and O (128 columns) fit twice.
+// Warps (384 threads):
+//   0-3, 4-7  softmax: tcgen05.ld of the row's 128 scores, maximum, O rescaled only
+//             when a row's maximum grows by more than 2^8, exponentials, P written
+//             over S (fp16 caches: one fp16 part, relative rounding 2^-11; bf16
+//             caches: bf16 hi + lo parts, 2^-17, so that V needs no conversion and
+//             has no range limit), handed over in two halves of 64 tokens;
+//   8, 9      tensor-core issue for w = 0, 1 (one thread each);
+//   10, 11    TMA: pair: warp 10 fills one ring of 5 stages for both; split: warp 10 + w
+//             fills w's own ring of 3.  Items alternate K(i), V(i): S has one
+//             buffer, so QK(i+1) follows PV(i) and consumption alternates too.
+// Barriers, per w: s_full (commit of QK(i)), p_half, p_full (4 warps each), o_done
+// (commit of PV(i)); per stage: full, free (one arrival a consumer).  Each is
+// waited on phase by phase by one role before that role enables the next phase,
+// so parities never alias: QK(i+1) waits for o_done(i) (PV(i) reads P from S's
+// columns), which needs p_full(i), which needs s_full(i) seen.  O may be
+// rescaled once s_full(i) is seen, since QK(i) was issued after o_done(i-1).
+// Every wait is bounded; a role that gives up raises the CTA's abort flag.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_decode.cuh"
+#include "pa_prefill.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+constexpr int kPrefixRows = 128;
+constexpr int kPrefixKv = 128;            // tokens of a K/V tile
+constexpr int kPrefixThreads = 384;
+constexpr int kPrefixMmaWarp = 8;
+constexpr int kPrefixLoadWarp = 10;
+constexpr int kPrefixStagesPair = 5;      // one ring
+constexpr int kPrefixStagesSplit = 3;     // each of two rings
+
+struct PrefixParams : SuffixParams {
+  int parts, part_tokens;   // partitions of the longest prefix; tokens of each (a multiple of 128)
+  int row_ctas;             // CTAs of 256 rows a (group, KV head, partition)
+};
+
+struct PrefixSmem {
+  static constexpr int kTile = 128 * 256;                  // [2 halves][128 rows][128 B]
+  static constexpr int kHalf = 128 * 128;
+  static constexpr int kTiles = 7;                         // pair: 2 Q + 5 stages; split: 1 Q + 2 x 3 stages
+  static constexpr int kBar = kTiles * kTile;
+  // full[6], free[6]; per w: s_full, p_half, p_full, o_done; drain
+  static constexpr int kNumBars = 12 + 8 + 1;
+  static constexpr int kTmemSlot = kBar + 8 * kNumBars;
+  static constexpr int kFlag = kTmemSlot + 4;
+  static constexpr int kBytes = kFlag + 4;
+  static constexpr int kAlloc = kBytes + 1024;             // + alignment of the base to 1024 B (swizzle atoms)
+};
+static_assert(PrefixSmem::kAlloc <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+static_assert(2 + kPrefixStagesPair <= PrefixSmem::kTiles && 1 + 2 * kPrefixStagesSplit <= PrefixSmem::kTiles, "tiles");
+
+// How many partials of the prefix a row has, from its place in the group: the
+// CTAs of its 256 rows run as "split" (two a partition) if the group has at most
+// 128 rows from the CTA's first on, else as "pair" (one).
+__device__ __forceinline__ bool prefix_split(int rows_in_group, int row_cta) {
+  return rows_in_group - row_cta * 2 * kPrefixRows <= kPrefixRows;
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+    pa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const PrefixParams p) {
+  using SM = PrefixSmem;
+  using PK = Pack16<T>;
+  constexpr int D = 128;
+  constexpr bool kLo = PK::kFormat == 1;   // bf16: P in two parts
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::kBar);
+  uint64_t *free_ = full + 6;
+  uint64_t *tile_bars = free_ + 6;   // w: s_full, p_half, p_full, o_done at 4 w
+  uint64_t *drain = tile_bars + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kTmemSlot);
+  volatile int *abort_s = reinterpret_cast<int *>(smem + SM::kFlag);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const long long cta = blockIdx.x;
+  const unsigned long long wait_limit = wait_limit_for(p.stall_cta, cta);
+  const bool stall_here = p.stall_cta != 0 && cta == p.stall_cta - 1;
+  if (warp == kPrefixLoadWarp && lane == 0) {
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- work item: blockIdx.x = ((group * row_ctas + rc) * Hkv + g) * parts + part
+  int item = blockIdx.x;
+  const int part = item % p.parts;
+  item /= p.parts;
+  const int g = item % p.num_kv_heads;
+  item /= p.num_kv_heads;
+  const int rc = item % p.row_ctas;
+  const int group = item / p.row_ctas;
+  const int s0 = p.group_start[group], s1 = p.group_start[group + 1];
+  const int prefix = p.prefix_lens[group];
+  if (s0 < 0 || s1 < s0 || s1 > p.num_seqs || s1 - s0 > p.max_group_size || prefix < 0 || prefix > p.max_prefix_len ||
+      prefix % kBlockSize != 0 || prefix / kBlockSize > p.max_blocks_per_seq) {
+    if (part == 0 && g == 0 && rc == 0 && tid == 0) record_error(8 /*PA_DEV_BAD_GROUP*/, group);
+    return;
+  }
+  const int rows_group = (s1 - s0) * G;
+  const int row0 = rc * 2 * kPrefixRows;
+  const int tok0 = part * p.part_tokens;
+  if (row0 >= rows_group || tok0 >= prefix) return;
+  const int tokens = min(p.part_tokens, prefix - tok0);
+  const int ntiles = (tokens + kPrefixKv - 1) / kPrefixKv;
+  const int nblk = tokens / kBlockSize;
+  const bool split = prefix_split(rows_group, rc);
+  const int32_t *bt_row = p.block_tables + static_cast<size_t>(s0) * p.max_blocks_per_seq + tok0 / kBlockSize;
+  // w's tiles: pair: 0 .. ntiles-1; split: w, w + 2, ...
+  auto tiles_of = [&](int w) { return split ? (ntiles - w + 1) / 2 : ntiles; };
+  // ring r: its first stage (barrier index, and tile of shared memory behind Q), and its length
+  const int q_tiles = split ? 1 : 2;
+  const int ring_len = split ? kPrefixStagesSplit : kPrefixStagesPair;
+  auto ring_base = [&](int w) { return split ? w * kPrefixStagesSplit : 0; };
+  auto stage_ptr = [&](int st) { return smem + (q_tiles + st) * SM::kTile; };
+
+  if (tid == 0) {
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&free_[i], split ? 1 : 2);   // one arrival per consuming issuer
+    }
+    for (int w = 0; w < 2; ++w) {
+      uint64_t *tb = tile_bars + 4 * w;
+      mbar_init(&tb[0], 1);   // s_full
+      mbar_init(&tb[1], 4);   // p_half
+      mbar_init(&tb[2], 4);   // p_full
+      mbar_init(&tb[3], 1);   // o_done
+    }
+    mbar_init(drain, 2);
+    fence_mbar_init();
+    *abort_s = 0;
+  }
+  if (warp == kPrefixMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // ---- Q -> shared memory, K-major 128-byte swizzled: [d half][row][128 B]; warpgroup w its tile
+  if (warp < kPrefixMmaWarp && (warp < 4 || !split)) {
+    const int w = warp >> 2;
+    uint8_t *q_s = smem + w * SM::kTile;
+    const T *qg = reinterpret_cast<const T *>(p.q);
+    const int c = tid & 15;
+    uint4 x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int row = ((tid & 127) >> 4) + 8 * k;
+      const int r = row0 + w * kPrefixRows + row;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows_group)
+        x[k] = *reinterpret_cast<const uint4 *>(
+            qg + (static_cast<size_t>(s0 + r / G) * p.num_heads + g * G + r % G) * D + c * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int row = ((tid & 127) >> 4) + 8 * k;
+      *reinterpret_cast<uint4 *>(q_s + (c >> 3) * SM::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[k];
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();   // barriers initialised, tensor memory allocated, Q in shared memory
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  int last_item[6];   // TMA warps: the last item issued into each stage of their ring (for the abort drain)
+#pragma unroll
+  for (int i = 0; i < 6; ++i) last_item[i] = -1;
+
+  if (warp >= kPrefixLoadWarp) {
+    // ================================================================ TMA producers
+    const int w = warp - kPrefixLoadWarp;
+    if (w == 0 || split) {
+      const int n = tiles_of(w);
+      const int base = ring_base(w);
+      int grp = -1, my_id = 0;
+      for (int it = 0; it < 2 * n; ++it) {   // item it: K (even) or V (odd) of this ring's tile it / 2
+        const int st = it % ring_len;
+        if (it >= ring_len &&
+            !__all_sync(kFullMask, mbar_wait_or_abort(&free_[base + st], (it / ring_len - 1) & 1, abort_s, wait_limit, true)))
+          break;
+        const int j = split ? 2 * (it >> 1) + w : it >> 1;
+        const int want = (8 * j) >> 5;
+        if (want != grp) {
+          grp = want;
+          const int lb = (grp << 5) + lane;
+          my_id = static_cast<int>(p.num_blocks);   // past the end of the pool: the box reads zeros
+          if (lb < nblk) {
+            const int v = bt_row[lb];
+            if (v < 0 || v >= p.num_blocks) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, v);
+            else my_id = v;
+          }
+        }
+        int ids[8];
+#pragma unroll
+        for (int bi = 0; bi < 8; ++bi) ids[bi] = __shfl_sync(kFullMask, my_id, (8 * j + bi) & 31);
+        const bool skip = stall_here && it == 0 && w == 0;   // test hook: K tile 0 left unissued
+        if (lane == 0 && !skip) {
+          uint8_t *dst = stage_ptr(base + st);
+          uint64_t *bar = &full[base + st];
+          const CUtensorMap *tm = (it & 1) ? &tm_v : &tm_k;
+          mbar_arrive_expect_tx(bar, SM::kTile);
+#pragma unroll
+          for (int bi = 0; bi < 8; ++bi)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              tma_load_5d(dst + half * SM::kHalf + bi * (kBlockSize * 128), tm, 0, half, g, 0, ids[bi], bar);
+        }
+        if (!skip) {
+#pragma unroll
+          for (int i = 0; i < 6; ++i)
+            if (i == st) last_item[i] = it;
+        }
+      }
+    }
+  } else if (warp >= kPrefixMmaWarp) {
+    if (lane == 0) {
+      // ================================================================ tensor-core issue
+      const int w = warp - kPrefixMmaWarp;
+      const int n = tiles_of(w);
+      const int base = ring_base(w);
+      uint64_t *tb = tile_bars + 4 * w;
+      constexpr uint32_t kIdescQK = instr_desc_f16(PK::kFormat, false, kPrefixRows, kPrefixKv);
+      constexpr uint32_t kIdescPV = instr_desc_f16(PK::kFormat, true, kPrefixRows, D);
+      bool ok = true;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!ok) return;
+        ok = mbar_test_wait(bar, parity) || mbar_wait_or_abort(bar, parity, abort_s, wait_limit);
+        if (!ok) {
+          record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
+          *abort_s = 1;
+        }
+        tc_fence_after();
+      };
+      const uint64_t a_qk = smem_desc_sw128(smem + (split ? 0 : w) * SM::kTile, 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(stage_ptr(base), 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(stage_ptr(base), SM::kHalf, 1024);
+      const uint32_t s_tmem = tmem + w * 256, o_tmem = s_tmem + 128;
+      for (int i = 0; i < n && ok; ++i) {
+        const int ik = 2 * i, iv = 2 * i + 1;
+        wait(&full[base + ik % ring_len], (ik / ring_len) & 1);
+        if (i > 0) wait(&tb[3], (i - 1) & 1);   // PV(i-1) has read P from S's columns
+        if (!ok) break;
+        const uint64_t b0 = k_desc + (((ik % ring_len) * SM::kTile) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16(s_tmem, a_qk + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4),
+                   b0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
+        umma_commit(&tb[0]);
+        umma_commit(&free_[base + ik % ring_len]);
+        wait(&full[base + iv % ring_len], (iv / ring_len) & 1);
+        if (!ok) break;
+        const uint64_t v0 = v_desc + (((iv % ring_len) * SM::kTile) >> 4);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          wait(&tb[1 + hf], i & 1);   // the half's P written
+          if (!ok) break;
+#pragma unroll
+          for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {   // 16 tokens = 8 columns of P a step
+            umma_f16_ts(o_tmem, s_tmem + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdescPV, i > 0 || kk > 0);
+            if constexpr (kLo) umma_f16_ts(o_tmem, s_tmem + 64 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&tb[3]);
+        umma_commit(&free_[base + iv % ring_len]);
+      }
+    }
+  } else {
+    // ================================================================ softmax warpgroup w
+    const int w = warp >> 2;
+    const int n = tiles_of(w);
+    const int r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + w * 256 + lane_base;
+    const uint32_t t_o = t_s + 128;
+    uint64_t *tb = tile_bars + 4 * w;
+    const float c2 = p.scale_log2;
+    float m_run = -INFINITY;   // reference maximum of this row's raw scores
+    float l_run = 0.f;         // sum of 2^((s - m_run) c2)
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!ok) return;
+      ok = __all_sync(kFullMask, mbar_wait_or_abort(bar, parity, abort_s, wait_limit));
+      if (!ok && lane == 0) {
+        record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
+        *abort_s = 1;
+      }
+      tc_fence_after();
+    };
+    for (int i = 0; i < n && ok; ++i) {
+      wait(&tb[0], i & 1);
+      if (!ok) break;
+      float s[128];
+      tmem_ld64(t_s, *reinterpret_cast<float (*)[64]>(s));
+      tmem_ld64(t_s + 64, *reinterpret_cast<float (*)[64]>(s + 64));
+      const int live = tokens - (split ? 2 * i + w : i) * kPrefixKv;   // a multiple of 16
+      if (live < kPrefixKv) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < live ? s[c] : -INFINITY;
+      }
+      float mx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx[k] = s[k];
+#pragma unroll
+      for (int c = 8; c < 128; ++c) mx[c & 7] = fmaxf(mx[c & 7], s[c]);
+      const float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+      bool need = false;
+      float f = 1.f;
+      if (i == 0) {
+        m_run = tmax;
+      } else if ((tmax - m_run) * c2 > kRescaleLog2) {
+        need = true;
+        f = ex2((m_run - tmax) * c2);
+        m_run = tmax;
+        l_run *= f;
+      }
+      if (__any_sync(kFullMask, need)) {   // PV(i-1) is complete: QK(i) was issued after it
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(t_o + c, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= f;
+          tmem_st32(t_o + c, o);
+        }
+      }
+      const float2 nmc = make_float2(-m_run * c2, -m_run * c2);
+      const float2 cc2 = make_float2(c2, c2);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t hi[32], lo[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 x = __ffma2_rn(make_float2(s[64 * hf + 2 * k], s[64 * hf + 2 * k + 1]), cc2, nmc);
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+          hi[k] = PK::pack(e.x, e.y);
+          if constexpr (kLo)
+            lo[k] = PK::pack(e.x - __uint_as_float(hi[k] << 16), e.y - __uint_as_float(hi[k] & 0xffff0000u));
+        }
+        tmem_st32u(t_s + 32 * hf, hi);
+        if constexpr (kLo) tmem_st32u(t_s + 64 + 32 * hf, lo);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tb[1 + hf]);
+      }
+      l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    }
+    // ---- this row's partial: m in base-2 units, o and l relative to it
+    if (n > 0) wait(&tb[3], (n - 1) & 1);
+    const int rg = row0 + (split ? 0 : w * kPrefixRows) + r;
+    if (ok && rg < rows_group) {
+      const size_t row = static_cast<size_t>(s0 + rg / G) * p.num_heads + g * G + rg % G;
+      const size_t slot = row * p.slots + (split ? 2 * part + w : part);
+      p.ws_m[slot] = n > 0 ? m_run * c2 : -INFINITY;
+      p.ws_l[slot] = l_run;
+    }
+    if (ok && n > 0) {
+      const bool stored = rg < rows_group;
+      const size_t row = static_cast<size_t>(s0 + (stored ? rg / G : 0)) * p.num_heads + g * G + rg % G;
+      float *dst = p.ws_o + (row * p.slots + (split ? 2 * part + w : part)) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(t_o + c, o);
+        if (stored) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4 *>(dst + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+
+  // ---- all roles done: tensor-core operations, their barrier arrivals and (after an
+  // abort) the copies in flight land before the memory is released, all bounded
+  __syncthreads();
+  if ((warp == kPrefixMmaWarp || warp == kPrefixMmaWarp + 1) && lane == 0) {
+    umma_commit(drain);
+    mbar_wait(drain, 0, wait_limit);
+  }
+  if (*abort_s && warp >= kPrefixLoadWarp && lane == 0) {
+    const int base = ring_base(warp - kPrefixLoadWarp);
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+      if (last_item[i] >= 0) mbar_wait(&full[base + i], (last_item[i] / ring_len) & 1, wait_limit);
+  }
+  __syncthreads();
+  if (warp == kPrefixMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Join of a row's prefix partials (slots 0 ..) and those of its own tokens (slot0 ..).
+template <typename T, int G>
+__global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const PrefixParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const long long rows = static_cast<long long>(p.num_seqs) * p.num_heads;
+  const long long step = static_cast<long long>(gridDim.x) * kReduceWarps;
+  for (long long row = static_cast<long long>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5); row < rows; row += step) {
+    const int b = static_cast<int>(row / p.num_heads);
+    const int L = p.context_lens[b];
+    const PrefixGroup group = group_of(p, b);
+    if (!group.ok || L < group.prefix || L - group.prefix > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize)
+      continue;   // recorded by the partition kernel; the row is left as it was
+    const int rows_group = (group.s1 - group.s0) * G;
+    const int rg = (b - group.s0) * G + static_cast<int>(row % p.num_heads) % G;
+    const int parts = (group.prefix + p.part_tokens - 1) / p.part_tokens;
+    const int na = prefix_split(rows_group, rg / (2 * kPrefixRows)) ? 2 * parts : parts;
+    join_row<T>(p, row, p.slots, na, p.slot0, (L - group.prefix + p.partition_size - 1) / p.partition_size);
+  }
+}
+
+}  // namespace pa
