@@ -1,0 +1,217 @@
+"""Shared-prefix decode against the plain 64-bit attention, over group sizes
+around the 128-row tiles, prefixes around the 128-token tiles, ragged and empty
+suffixes, and its error paths."""
+import pytest
+import torch
+
+import step_reference as ref
+
+pytestmark = pytest.mark.gpu
+P_BITS = {"f16": 11, "bf16": 16}     # the prefix's softmax weights: one fp16 part, two bf16 parts
+
+
+@pytest.fixture(scope="module")
+def pa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_464_b200 import capi
+    capi.get_device_error(clear=True)
+    yield capi
+    code, detail = capi.get_device_error(clear=True)
+    assert code == 0, (code, detail)
+
+
+def make(sizes, prefixes, suffix, hkv, G, ty, seed):
+    starts, lens, shared = [0], [], []
+    for size, prefix in zip(sizes, prefixes):
+        first = starts[-1]
+        lens += [prefix + suffix(first + i) for i in range(size)]
+        shared.append((first, first + size, prefix))
+        starts.append(first + size)
+    k, v, tables, lens = ref.make_cache(lens, hkv, ty, seed=seed, shared=shared)
+    q = ref.make_q(len(lens), hkv * G, ty, seed=seed)
+    gs, pl = torch.tensor(starts, dtype=torch.int32), torch.tensor(prefixes, dtype=torch.int32)
+    # the prefix entries of a group's other rows are not read
+    blind = tables.clone()
+    for first, last, prefix in shared:
+        blind[first + 1:last, :prefix // 16] = -5
+    return q, k, v, tables, blind, lens, gs, pl
+
+
+def check(pa, sizes, prefixes, suffix, hkv, G, ty, seed, scale=0.088):
+    q, k, v, tables, blind, lens, gs, pl = make(sizes, prefixes, suffix, hkv, G, ty, seed)
+    want, weight = ref.attention(q, k, v, tables, lens, scale)
+    args = [t.cuda() for t in (q, k, v, blind, lens, gs, pl)]
+    out = torch.full_like(args[0], float("nan"))
+    pa.decode_shared_prefix(*args, scale, out)
+    err = (out.cpu().double() - want).abs()
+    tol = ref.attention_tolerance(want, weight, ty, P_BITS[ty])
+    assert (err <= tol).all(), (err - tol).max()
+    assert torch.equal(pa.decode_shared_prefix(*args, scale), out)      # the same bits again
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("size", [1, 2, 16, 17, 33])
+def test_group_sizes(pa, ty, G, size):
+    check(pa, [size], [272], lambda b: (7 * b) % 40, 2, G, ty, seed=size + G)
+
+
+@pytest.mark.parametrize("ty,G,size", [("bf16", 8, 31), ("bf16", 8, 32), ("bf16", 8, 48), ("bf16", 8, 49),
+                                       ("f16", 1, 127), ("f16", 1, 129), ("f16", 1, 256), ("f16", 1, 257),
+                                       ("bf16", 2, 193)])
+def test_row_tile_edges(pa, ty, G, size):
+    """Rows 128, 256 and 384 are where a CTA's warpgroups change from sharing rows to sharing tiles."""
+    check(pa, [size], [400], lambda b: 1 + b % 5, 1, G, ty, seed=size)
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+@pytest.mark.parametrize("prefix", [0, 16, 112, 128, 144, 256, 272, 640, 2048, 5008])
+@pytest.mark.parametrize("size", [3, 40])
+def test_prefix_lengths(pa, ty, prefix, size):
+    check(pa, [size], [prefix], lambda b: b % 18, 1, 4, ty, seed=prefix + size)
+
+
+def test_suffix_longer_than_a_partition(pa):
+    check(pa, [5], [160], lambda b: [0, 1, 1024, 1025, 2300][b], 2, 4, "bf16", seed=1)
+
+
+def test_several_groups(pa):
+    """Unequal groups, an empty one, one without a prefix, one of a single sequence, rows without any token."""
+    check(pa, [9, 0, 70, 1, 4], [128, 512, 336, 1040, 0], lambda b: [0, 3, 16, 55][b % 4], 2, 4, "bf16", seed=2)
+
+
+def test_many_groups(pa):
+    check(pa, [1 + i % 3 for i in range(70)], [16 * (i % 5) for i in range(70)], lambda b: b % 21, 1, 2, "f16", seed=3)
+
+
+def test_growing_maxima_rescale(pa):
+    """Keys that grow along the prefix: every tile's maximum is far above the last one's."""
+    for ty in ("bf16", "f16"):
+        for size in (3, 60):
+            q, k, v, tables, _, lens, gs, pl = make([size], [1536], lambda b: 20, 1, 4, ty, seed=4)
+            grow = (torch.arange(96) // 8 + 1).to(k.dtype)
+            k[tables[0, :96].long()] *= grow[:, None, None, None]
+            want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+            out = pa.decode_shared_prefix(*[t.cuda() for t in (q, k, v, tables, lens, gs, pl)], 0.088).cpu()
+            # scores up to 12 times larger than attention_tolerance counts on
+            tol = ref.attention_tolerance(want, 12 * weight, ty, P_BITS[ty])
+            assert ((out.double() - want).abs() <= tol).all()
+
+
+def test_no_range_limit_on_values(pa):
+    """bf16 values far outside what fp16 holds."""
+    q, k, v, tables, _, lens, gs, pl = make([40], [256], lambda b: 9, 1, 4, "bf16", seed=5)
+    for factor in (2.0 ** 60, 2.0 ** -60):
+        x = v * factor
+        want, weight = ref.attention(q, k, x, tables, lens, 0.088)
+        out = pa.decode_shared_prefix(*[t.cuda() for t in (q, k, x, tables, lens, gs, pl)], 0.088).cpu()
+        tol = ref.attention_tolerance(want, weight, "bf16", 16) - 1e-7     # relative alone
+        assert ((out.double() - want).abs() <= tol).all()
+
+
+def test_live_nan_reaches_its_group_only(pa):
+    q, k, v, tables, _, lens, gs, pl = make([5, 6], [256, 256], lambda b: 9, 1, 4, "bf16", seed=5)
+    v[tables[0, 3], 2, 0, 17] = float("nan")
+    out = pa.decode_shared_prefix(*[t.cuda() for t in (q, k, v, tables, lens, gs, pl)], 0.088).cpu()
+    assert out[:5, :, 17].isnan().all() and int(out.isnan().sum()) == 5 * 4
+
+
+def test_agrees_with_decode(pa):
+    from paged_kv_cache_464_b200 import inputs
+    case = inputs.make_case("shared_prefix", lens=[1040, 1300, 1536, 1100, 1025] * 7)
+    d = "cuda"
+    # the workload's copy-on-write destinations hold what the shared block holds
+    args = [case.q.to(d), case.k_cache_post.to(d), case.v_cache_post.to(d), case.block_tables.to(d),
+            case.context_lens.to(d)]
+    gs = torch.tensor([0, 35], dtype=torch.int32, device=d)
+    pl = torch.tensor([1024], dtype=torch.int32, device=d)
+    out = pa.decode_shared_prefix(*args, gs, pl, case.scale).double()
+    dense = pa.decode(*args, case.scale, max_context_len=case.max_context_len).double()
+    assert ((out - dense).abs() <= 2e-3 + 1e-2 * dense.abs()).all()
+
+
+@pytest.mark.expects_device_error
+def test_bad_groups_and_lengths_are_reported(pa):
+    q, k, v, tables, _, lens, gs, pl = make([3, 4], [128, 160], lambda b: 9, 1, 4, "bf16", seed=6)
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    tol = ref.attention_tolerance(want, weight, "bf16", 16)
+
+    def call(gs=gs, pl=pl, lens=lens, tables=tables, mp=160, ms=9, mg=4):
+        out = torch.full_like(q, 6.0).cuda()
+        pa.decode_shared_prefix(*[t.cuda() for t in (q, k, v, tables, lens, gs, pl)], 0.088, out, max_prefix_len=mp,
+                                max_suffix_len=ms, max_group_size=mg)
+        out = out.cpu()
+        kept = [b for b in range(7) if (out[b] == 6.0).all()]
+        fine = [b for b in range(7) if ((out[b].double() - want[b]).abs() <= tol[b]).all()]
+        return kept, fine, pa.get_device_error(clear=True)
+
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32)
+
+    first, second = [0, 1, 2], [3, 4, 5, 6]
+    assert call() == ([], first + second, (0, 0))
+    assert call(pl=i32(128, 150)) == (second, first, (8, 1))         # not a multiple of 16
+    assert call(pl=i32(-16, 160)) == (first, second, (8, 0))
+    assert call(mp=144) == (second, first, (8, 1))                   # beyond the bound
+    assert call(mg=3) == (second, first, (8, 1))
+    assert call(gs=i32(0, 3, 8)) == (second, first, (8, 1))          # past the batch
+    kept, fine, err = call(gs=i32(1, 3, 7))                          # sequence 0 is in no group
+    assert kept == [0] and err == (8, -1) and set(second) <= set(fine)
+    short = lens.clone()
+    short[1], short[5] = 100, -2                                     # shorter than the prefix
+    kept, fine, err = call(lens=short)
+    assert kept == [1, 5] and fine == [0, 2, 3, 4, 6] and err[0] == 4 and err[1] in (1, 5)
+    assert call(ms=8)[0] == first + second
+    t = tables.clone()
+    t[0, 2] = 10 ** 6
+    kept, fine, err = call(tables=t)
+    assert kept == [] and err == (1, 10 ** 6) and set(second) <= set(fine)
+
+
+@pytest.mark.expects_device_error
+def test_wait_that_runs_out_is_reported(pa):
+    """One CTA of the prefix kernel leaves its first K tile unissued: it gives up, the context stays usable."""
+    for size in (4, 60):
+        q, k, v, tables, _, lens, gs, pl = make([size], [1024], lambda b: 9, 1, 4, "bf16", seed=7)
+        args = [t.cuda() for t in (q, k, v, tables, lens, gs, pl)]
+        pa.test_stall_next_launch("shared_prefix", 1)
+        pa.decode_shared_prefix(*args, 0.088)
+        assert pa.get_device_error(clear=True) == (5, 1)
+        want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+        out = pa.decode_shared_prefix(*args, 0.088).cpu()
+        assert ((out.double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 16)).all()
+
+
+def test_guard_bands(pa):
+    """Nothing is written outside out and the workspace."""
+    q, k, v, tables, blind, lens, gs, pl = make([33, 5], [272, 144], lambda b: b % 20, 2, 4, "f16", seed=8)
+    S, hq, d = q.shape
+    qd, kd, vd, td, ld, gd, pd = [t.cuda() for t in (q, k, v, blind, lens, gs, pl)]
+    need = pa.decode_shared_prefix_workspace_bytes(S, 2, hq, 2, d, 272, 19, 33)
+    pad = 4096
+    buf = torch.full((need + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    room = torch.full((S * hq * d + 2 * pad,), 11.0, dtype=torch.half, device="cuda")
+    out = room[pad:-pad].view(S, hq, d)
+    kb, vb = kd.clone(), vd.clone()
+    pa.decode_shared_prefix(qd, kd, vd, td, ld, gd, pd, 0.088, out, max_prefix_len=272, max_suffix_len=19,
+                            max_group_size=33, workspace=buf[pad:pad + need])
+    assert (buf[:pad] == 0xA5).all() and (buf[pad + need:] == 0xA5).all()
+    assert (room[:pad] == 11.0).all() and (room[-pad:] == 11.0).all()
+    assert torch.equal(kb.view(torch.int16), kd.view(torch.int16)) and torch.equal(vb.view(torch.int16), vd.view(torch.int16))
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    assert ((out.cpu().double() - want).abs() <= ref.attention_tolerance(want, weight, "f16", 11)).all()
+
+
+def test_blocks_past_four_gigabytes(pa):
+    blocks, hkv = (1 << 17) + 60, 8
+    k = torch.zeros((blocks, 16, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    q, ks, vs, tables, _, lens, gs, pl = make([6], [256], lambda b: 30, hkv, 4, "bf16", seed=9)
+    n = ks.shape[0]
+    far = tables.clone()
+    far[far >= 0] += blocks - n
+    k[blocks - n:], v[blocks - n:] = ks.cuda(), vs.cuda()
+    out = pa.decode_shared_prefix(q.cuda(), k, v, far.cuda(), lens.cuda(), gs.cuda(), pl.cuda(), 0.088).cpu()
+    want, weight = ref.attention(q, ks, vs, tables, lens, 0.088)
+    assert ((out.double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 16)).all()

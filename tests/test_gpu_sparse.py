@@ -1,0 +1,273 @@
+"""Block bounds (bit-exact), block choice (equal, ties to the lowest block) and
+decode over chosen blocks (within rounding) against plain 64-bit forms."""
+import pytest
+import torch
+
+import step_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_464_b200 import capi
+    capi.get_device_error(clear=True)
+    yield capi
+    code, detail = capi.get_device_error(clear=True)
+    assert code == 0, (code, detail)
+
+
+def cuda(*ts):
+    return [t.cuda() for t in ts]
+
+
+LENS = [1, 0, 15, 16, 17, 33, 250, 31, 64, 129]
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hkv", [1, 3, 8])
+@pytest.mark.parametrize("new", ["one", "all", "some"])
+def test_bounds(pa, ty, hkv, new):
+    k, _, tables, lens = ref.make_cache(LENS, hkv, ty, seed=hkv)
+    n = {"one": lens.clamp(max=1), "all": lens, "some": torch.tensor([0, 0, 15, 2, 2, 20, 100, 16, 33, 1], dtype=torch.int32)}[new]
+    bounds = torch.full((k.shape[0], 2, hkv, k.shape[3]), 9.0, dtype=k.dtype)
+    want = ref.block_bounds(k, bounds, tables, lens, n)
+    kd, bd, td, ld, nd = cuda(k, bounds, tables, lens, n)
+    pa.update_block_bounds(kd, bd, td, ld, nd, max_new_len=int(n.max()))
+    assert torch.equal(bd.cpu(), want)
+    bd2 = bounds.cuda()
+    pa.update_block_bounds(kd, bd2, td, ld, nd)         # the maximum read from the device
+    assert torch.equal(bd2, bd)
+
+
+def test_bounds_keep_nan_and_infinity(pa):
+    k, _, tables, lens = ref.make_cache([40], 2, "bf16", seed=1)
+    k[tables[0, 0], 3, 0, 5] = float("nan")
+    k[tables[0, 1], 2, 1, 7] = float("-inf")
+    kd, td, ld = cuda(k, tables, lens)
+    bd = torch.zeros((k.shape[0], 2, 2, 128), dtype=k.dtype, device="cuda")
+    pa.update_block_bounds(kd, bd, td, ld, ld, max_new_len=40)
+    b = bd.cpu()
+    assert b[tables[0, 0], :, 0, 5].isnan().all() and int(b.isnan().sum()) == 2
+    assert b[tables[0, 1], 0, 1, 7] == float("-inf") and b[tables[0, 1], 1, 1, 7].isfinite()
+
+
+@pytest.mark.expects_device_error
+def test_bounds_report_bad_input(pa):
+    k, _, tables, lens = ref.make_cache([40, 40, 40], 1, "bf16", seed=2)
+    good = ref.block_bounds(k, torch.zeros((k.shape[0], 2, 1, 128), dtype=k.dtype), tables, lens, lens)
+    kd, ld = cuda(k, lens)
+
+    def call(tables, new, lens=ld, most=40):
+        bd = torch.zeros((k.shape[0], 2, 1, 128), dtype=k.dtype, device="cuda")
+        pa.update_block_bounds(kd, bd, tables.cuda(), lens, torch.tensor(new, dtype=torch.int32, device="cuda"), max_new_len=most)
+        return bd.cpu(), pa.get_device_error(clear=True)
+
+    for new, seq in (([40, 41, 40], 1), ([40, 40, -1], 2)):
+        b, err = call(tables, new)
+        assert err == (4, seq)
+        for s in range(3):
+            same = torch.equal(b[tables[s, :3].long()], good[tables[s, :3].long()])
+            assert same == (s != seq)
+    assert call(tables, [40, 40, 40], most=39)[1][0] == 4
+    t = tables.clone()
+    t[1, 1] = k.shape[0]
+    assert call(t, [40, 40, 40])[1] == (1, k.shape[0])
+    long = ld.clone()
+    long[0] = tables.shape[1] * 16 + 1
+    assert call(tables, [1, 1, 1], lens=long)[1] == (4, 0)
+
+
+def bounds_of(k, tables, lens):
+    return ref.block_bounds(k, torch.zeros((k.shape[0], 2, *k.shape[2:]), dtype=k.dtype), tables, lens, lens)
+
+
+SELECT_LENS = [0, 1, 16, 17, 63, 64, 65, 333, 1024, 4097]
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hkv,G", [(1, 1), (3, 2), (2, 4), (2, 8)])
+@pytest.mark.parametrize("K,sink,recent", [(1, 0, 1), (4, 1, 1), (5, 2, 3), (37, 0, 0), (300, 1, 4)])
+def test_choice(pa, ty, hkv, G, K, sink, recent):
+    k, _, tables, lens = ref.make_cache(SELECT_LENS, hkv, ty, seed=hkv * 10 + G)
+    q = ref.make_q(len(lens), hkv * G, ty, seed=K)
+    bounds = bounds_of(k, tables, lens)
+    want = ref.choose(q, bounds, tables, lens, K, sink, recent)
+    got = pa.select_blocks(*cuda(q, bounds, tables, lens), K, sink_blocks=sink, recent_blocks=recent)
+    assert torch.equal(got.cpu(), want)
+
+
+def test_choice_ties_go_to_the_lowest_block(pa):
+    """Blocks with the same bounds, all of them or in turn, and whole-number scores."""
+    hkv, G, n = 2, 4, 400
+    lens = torch.tensor([n * 16], dtype=torch.int32)
+    tables = torch.arange(n, dtype=torch.int32)[None]
+    g = torch.Generator().manual_seed(1)
+    q = torch.randint(-2, 3, (1, hkv * G, 128), generator=g).bfloat16()
+    for kinds in (1, 2, 7):
+        base = torch.randint(-2, 3, (kinds, 2, hkv, 128), generator=g)
+        base = torch.stack([base.amin(1), base.amax(1)], 1)
+        bounds = base[torch.arange(n) % kinds].bfloat16()
+        for K, sink, recent in ((3, 0, 0), (9, 1, 1), (150, 2, 5), (399, 0, 1), (6, 3, 3)):
+            want = ref.choose(q, bounds, tables, lens, K, sink, recent)
+            got = pa.select_blocks(*cuda(q, bounds, tables, lens), K, sink_blocks=sink, recent_blocks=recent)
+            assert torch.equal(got.cpu(), want), (kinds, K)
+
+
+def test_choice_near_ties_are_ordered_in_64_bits(pa):
+    """Scores of about 2^12 that differ by 2^-14: 26 bits apart, which no fp32 sum can order."""
+    n = 64
+    lens = torch.tensor([n * 16], dtype=torch.int32)
+    tables = torch.arange(n, dtype=torch.int32)[None]
+    q = torch.ones((1, 1, 128), dtype=torch.float32)[..., :64].contiguous()
+    q[0, 0, 0] = 2.0 ** -20
+    hi = torch.full((n, 64), 64.0)
+    step = torch.randperm(n, generator=torch.Generator().manual_seed(4))
+    hi[:, 0] = step.float() * 64          # adds step * 2^-14
+    bounds = torch.stack([-hi, hi], 1)[:, :, None].contiguous()
+    got = pa.select_blocks(*cuda(q, bounds, tables, lens), 8, sink_blocks=0, recent_blocks=0)
+    want = torch.argsort(step, descending=True)[:8].sort().values.int()
+    assert torch.equal(got.cpu()[0, 0], want)
+
+
+def test_choice_takes_nan_blocks_first(pa):
+    k, _, tables, lens = ref.make_cache([1000], 1, "bf16", seed=4)
+    bounds = bounds_of(k, tables, lens)
+    for j in (11, 40):
+        bounds[tables[0, j], 0, 0, 9] = bounds[tables[0, j], 1, 0, 9] = float("nan")
+    bounds[tables[0, 20], 1, 0, 3] = float("inf")
+    q = ref.make_q(1, 8, "bf16", seed=1)
+    want = ref.choose(q, bounds, tables, lens, 5, 0, 0)
+    got = pa.select_blocks(*cuda(q, bounds, tables, lens), 5, sink_blocks=0, recent_blocks=0).cpu()
+    assert torch.equal(got, want) and {11, 20, 40} <= set(got[0, 0].tolist())
+
+
+@pytest.mark.expects_device_error
+def test_choice_reports_bad_input(pa):
+    k, _, tables, lens = ref.make_cache([200, 300], 1, "bf16", seed=4)
+    bounds = bounds_of(k, tables, lens)
+    q = ref.make_q(2, 4, "bf16", seed=1)
+    want = ref.choose(q, bounds, tables, lens, 5, 1, 1)
+    qd, bd, td = cuda(q, bounds, tables)
+    for bad in (-1, 301):
+        l2 = lens.clone()
+        l2[0] = bad
+        got = pa.select_blocks(qd, bd, td, l2.cuda(), 5, max_context_len=300).cpu()
+        assert pa.get_device_error(clear=True) == (4, 0)
+        assert (got[0] == -1).all() and torch.equal(got[1], want[1])
+    t = tables.clone()
+    t[1, 2] = -7
+    pa.select_blocks(qd, bd, t.cuda(), lens.cuda(), 5, max_context_len=300)
+    assert pa.get_device_error(clear=True) == (1, -7)
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hkv,G", [(1, 1), (3, 2), (2, 4), (2, 8)])
+@pytest.mark.parametrize("K", [1, 4, 9, 70])
+def test_decode_over_chosen_blocks(pa, ty, hkv, G, K):
+    lens = [0, 1, 16, 17, 63, 333, 1024, 40]
+    k, v, tables, lens = ref.make_cache(lens, hkv, ty, seed=K)
+    q = ref.make_q(len(lens), hkv * G, ty, seed=K)
+    g = torch.Generator().manual_seed(K)
+    chosen = torch.full((len(lens), hkv, K), -1, dtype=torch.int32)
+    for b in range(len(lens)):
+        n = -(-int(lens[b]) // 16)
+        for h in range(hkv):
+            m = min(K, n)
+            if b == 7 and h == 0:
+                m = 0                      # a list that names no block
+            pick = torch.randperm(n, generator=g)[:m].int()     # any order, holes between
+            at = torch.randperm(K, generator=g)[:m]
+            chosen[b, h, at] = pick
+    scale = q.shape[2] ** -0.5
+    want, weight = ref.attention(q, k, v, tables, lens, scale, chosen)
+    out = torch.full_like(q, 4.0).cuda()
+    qd, kd, vd, td, ld, cd = cuda(q, k, v, tables, lens, chosen)
+    pa.decode_selected(qd, kd, vd, td, ld, cd, scale, out)
+    err = (out.cpu().double() - want).abs()
+    # 16-bit grouped heads: P in two parts of bf16 (2^-16 and less); fp32: none
+    tol = ref.attention_tolerance(want, weight, ty, 16)
+    assert (err <= tol).all(), (err - tol).max()
+    assert (out.cpu()[0] == 0).all() and (out.cpu()[7, :G] == 0).all()
+    again = pa.decode_selected(qd, kd, vd, td, ld, cd, scale)
+    assert torch.equal(again, out)
+
+
+def test_every_block_chosen_is_decode(pa):
+    k, v, tables, lens = ref.make_cache([700, 33, 1500], 8, "bf16", seed=3)
+    q = ref.make_q(3, 32, "bf16", seed=3)
+    qd, kd, vd, td, ld = cuda(q, k, v, tables, lens)
+    bd = torch.zeros((k.shape[0], 2, 8, 128), dtype=k.dtype, device="cuda")
+    pa.update_block_bounds(kd, bd, td, ld, ld, max_new_len=1500)
+    chosen = pa.select_blocks(qd, bd, td, ld, 100, max_context_len=1500)
+    out = pa.decode_selected(qd, kd, vd, td, ld, chosen, 0.088)
+    dense = pa.decode(qd, kd, vd, td, ld, 0.088, max_context_len=1500)
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    tol = ref.attention_tolerance(want, weight, "bf16", 16)
+    assert ((out.cpu().double() - want).abs() <= tol).all() and ((dense.cpu().double() - want).abs() <= tol).all()
+
+
+def test_live_nan_reaches_the_output(pa):
+    k, v, tables, lens = ref.make_cache([200], 1, "bf16", seed=3)
+    v[tables[0, 5], 2, 0, 17] = float("nan")
+    k2 = k.clone()
+    k2[tables[0, 5]] = float("nan")
+    q = ref.make_q(1, 4, "bf16", seed=3)
+    chosen = torch.tensor([[[2, 5, -1]]], dtype=torch.int32)
+    out = pa.decode_selected(*cuda(q, k, v, tables, lens, chosen), 0.088).cpu()
+    assert out[0, :, 17].isnan().all() and int(out.isnan().sum()) == 4
+    assert pa.decode_selected(*cuda(q, k2, v, tables, lens, chosen), 0.088).isnan().all()
+    only = torch.tensor([[[5, -1, -1]]], dtype=torch.int32)
+    assert pa.decode_selected(*cuda(q, k2, v, tables, lens, only), 0.088).isnan().all()
+    apart = torch.tensor([[[2, 7, -1]]], dtype=torch.int32)     # the NaN block is not named
+    assert pa.decode_selected(*cuda(q, k2, v, tables, lens, apart), 0.088).isfinite().all()
+
+
+@pytest.mark.expects_device_error
+def test_decode_selected_reports_bad_entries(pa):
+    k, v, tables, lens = ref.make_cache([100, 64], 1, "bf16", seed=3)
+    q = ref.make_q(2, 4, "bf16", seed=3)
+    good = torch.tensor([[[0, 3, 6]], [[1, 2, -1]]], dtype=torch.int32)
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088, good)
+    tol = ref.attention_tolerance(want, weight, "bf16", 16)
+    qd, kd, vd, td, ld = cuda(q, k, v, tables, lens)
+    bad = good.clone()
+    bad[1, 0, 2] = 4                   # the sequence has four blocks: 0 .. 3
+    out = pa.decode_selected(qd, kd, vd, td, ld, bad.cuda(), 0.088).cpu()
+    assert pa.get_device_error(clear=True) == (1, 4)
+    assert ((out.double() - want).abs() <= tol).all()       # the entry counts for nothing
+    t = tables.clone()
+    t[0, 3] = 10 ** 6
+    pa.decode_selected(qd, kd, vd, t.cuda(), ld, good.cuda(), 0.088)
+    assert pa.get_device_error(clear=True) == (1, 10 ** 6)
+    l2 = ld.clone()
+    l2[0] = -3
+    out = torch.full_like(qd, 2.0)
+    pa.decode_selected(qd, kd, vd, td, l2, good.cuda(), 0.088, out)
+    assert pa.get_device_error(clear=True) == (4, 0)
+    assert (out[0] == 2.0).all() and ((out[1].cpu().double() - want[1]).abs() <= tol[1]).all()
+
+
+def test_blocks_past_four_gigabytes(pa):
+    blocks, hkv = (1 << 17) + 40, 8
+    k = torch.zeros((blocks, 16, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    bounds = torch.zeros((blocks, 2, hkv, 128), dtype=torch.bfloat16, device="cuda")
+    ks, vs, tables, lens = ref.make_cache([500], hkv, "bf16", seed=8)
+    far = tables.clone()
+    n = ks.shape[0]
+    far[far >= 0] += blocks - n
+    k[blocks - n:], v[blocks - n:] = ks.cuda(), vs.cuda()
+    q = ref.make_q(1, 32, "bf16", seed=8)
+    fd, ld, qd = cuda(far, lens, q)
+    pa.update_block_bounds(k, bounds, fd, ld, ld, max_new_len=500)
+    want_b = bounds_of(ks, tables, lens)
+    assert torch.equal(bounds[blocks - n:].cpu(), want_b)
+    assert int((bounds[:blocks - n] != 0).sum()) == 0
+    chosen = pa.select_blocks(qd, bounds, fd, ld, 7, max_context_len=500)
+    assert torch.equal(chosen.cpu(), ref.choose(q, want_b, tables, lens, 7, 1, 1))
+    out = pa.decode_selected(qd, k, v, fd, ld, chosen, 0.088)
+    want, weight = ref.attention(q, ks, vs, tables, lens, 0.088, chosen.cpu())
+    assert ((out.cpu().double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 16)).all()
