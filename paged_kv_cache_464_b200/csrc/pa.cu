@@ -872,7 +872,7 @@ pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa
   pa::SuffixParams sp = p;
   sp.stall_cta = 0;
   st = launch(suffix, dim3((unsigned)grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, sp);
-  if (st != PA_OK) return st;
+  if (st != PA_OK || p.max_partitions == 1) return st;
   const long long rows = (long long)p.num_seqs * p.num_heads;
   long long ctas = (rows + pa::kReduceWarps - 1) / pa::kReduceWarps;
   if (ctas > 8LL * sm_count()) ctas = 8LL * sm_count();

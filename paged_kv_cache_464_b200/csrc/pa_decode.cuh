@@ -102,13 +102,20 @@ struct DecodeParams {
 //   kWalkSelected  the tokens of the blocks that a list names, one list for each
 //                  (sequence, KV head) (pa_decode_selected)
 constexpr int kWalkAll = 0, kWalkSuffix = 1, kWalkSelected = 2;
+constexpr int kJoinBatch = 4;   // kWalkSuffix: the prefix's partials in flight per thread when it combines
 
 struct SuffixParams : DecodeParams {   // context_lens: whole lengths; max_context_len: of the suffix
   const int32_t *group_start;     // [num_groups + 1]
   const int32_t *prefix_lens;     // [num_groups]
   int num_groups, max_prefix_len, max_group_size;
+  int parts, part_tokens;         // partitions of the longest prefix (0: no prefix kernel); tokens of each
   int slots, slot0;               // partials of a row in the workspace; the first of the suffix's
 };
+
+// Workspace rows of a (KV head, slot): the S * G (sequence, grouped head) rows, consecutive.
+__device__ __forceinline__ size_t prefix_slot(const SuffixParams &p, int g, int slot) {
+  return (static_cast<size_t>(g) * p.slots + slot) * p.num_seqs * (p.num_heads / p.num_kv_heads);
+}
 
 struct SelectedParams : DecodeParams {
   const int32_t *selected;        // [S][Hkv][num_selected] logical blocks; < 0: no block
@@ -155,6 +162,22 @@ __device__ __forceinline__ PrefixGroup group_of(const SuffixParams &p, int b) {
            r.prefix / kBlockSize <= p.max_blocks_per_seq;
   }
   return r;
+}
+
+// The CTA of the prefix kernel that has a group's rows row0 .. row0 + 255 runs as
+// "split" (its two warpgroups share the rows, and leave a partial each) if at most
+// 128 of them exist, else as "pair" (128 rows, one partial each).
+constexpr int kPrefixRows = 128;
+__device__ __forceinline__ bool prefix_split(int rows_in_group, int row_cta) {
+  return rows_in_group - row_cta * 2 * kPrefixRows <= kPrefixRows;
+}
+
+// How many partials of the prefix the row of sequence b and grouped head hh has.
+template <int G>
+__device__ __forceinline__ int prefix_partials(const SuffixParams &p, const PrefixGroup &group, int b, int hh) {
+  const int parts = (group.prefix + p.part_tokens - 1) / p.part_tokens;
+  const int row = (b - group.s0) * G + hh;
+  return prefix_split((group.s1 - group.s0) * G, row / (2 * kPrefixRows)) ? 2 * parts : parts;
 }
 
 // Byte offset of 16-byte chunk `c` (0..15) of token `t` in a swizzled tile.
@@ -793,6 +816,19 @@ __global__ void __launch_bounds__(256) zero_counts_kernel(unsigned *count, int n
 // default launch shape), or six of the two-warp shape.
 constexpr int decode_min_ctas(int warps) { return warps == 2 ? 6 : PA_DECODE_MIN_CTAS_PER_SM; }
 
+struct WaitAtExit {
+  bool on;
+  __device__ __forceinline__ ~WaitAtExit() {
+    if (on) pdl_wait();
+  }
+};
+
+template <int kWalk>
+__device__ __forceinline__ bool waits_late(const typename WalkParams<kWalk>::type &p) {
+  if constexpr (kWalk == kWalkSuffix) return p.parts > 0;
+  return false;
+}
+
 template <typename T, int G, typename Math, int W = kDecodeWarps, int kWalk = kWalkAll>
 __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     pa_decode_partition_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -817,7 +853,12 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
   const int lane = threadIdx.x & 31;
   const unsigned long long wait_limit = wait_limit_for(p.stall_cta, blockIdx.x);
   const bool stall_here = p.stall_cta != 0 && static_cast<int>(blockIdx.x) == p.stall_cta - 1;
-  pdl_wait();      // the previous kernel's writes (caches, inputs) are visible from here on
+  // The suffix walk behind a prefix kernel needs nothing of that one until it combines
+  // the two, and what ran before the prefix kernel was complete when that one let this
+  // grid start; so it waits last (and on every way out: its end is the call's end).
+  const bool late = waits_late<kWalk>(p);
+  const WaitAtExit wait_at_exit{late};
+  if (!late) pdl_wait();      // the previous kernel's writes (caches, inputs) are visible from here on
   pdl_trigger();   // the reduce kernel may be scheduled once every CTA of this grid has started
 
   // ---- work item: blockIdx.x = ((b * Hkv) + g) * NPmax + part
@@ -828,8 +869,9 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
   const int b = item / p.num_kv_heads;
   int L = p.context_lens[b];
   int block0 = 0;   // first logical block walked
+  PrefixGroup group{};
   if constexpr (kWalk == kWalkSuffix) {
-    const PrefixGroup group = group_of(p, b);
+    group = group_of(p, b);
     if (!group.ok) {
       if (part == 0 && g == 0 && threadIdx.x == 0) record_error(8 /*PA_DEV_BAD_GROUP*/, group.index);
       return;
@@ -843,10 +885,12 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     return;
   }
   const int P = p.partition_size;
-  const int nparts = kWalk == kWalkSelected ? p.max_partitions : (L + P - 1) / P;
+  // the last launch of a shared-prefix call when no row has more than one partition
+  const bool joins = kWalk == kWalkSuffix && p.max_partitions == 1;
+  const int nparts = kWalk == kWalkSelected ? p.max_partitions : joins ? 1 : (L + P - 1) / P;
   const int h0 = g * G;   // first query head of this KV head (contiguous groups)
   T *out = reinterpret_cast<T *>(p.out) + (static_cast<size_t>(b) * p.num_heads + h0) * D;
-  if (L == 0) {   // empty context: the row is the empty sum, zeros
+  if (L == 0 && !joins) {   // empty context: the row is the empty sum, zeros
     if (part == 0 && kWalk != kWalkSuffix)
       for (int i = threadIdx.x * 4; i < G * D; i += (W * 32) * 4) Elem<T>::store4(out + i, 0.f, 0.f, 0.f, 0.f);
     return;
@@ -1003,7 +1047,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (kWalk == kWalkSelected && m_s[w * G + hh] == -INFINITY && l_s[w * G + hh] == 0.f) continue;   // no block
+      if (kWalk != kWalkAll && m_s[w * G + hh] == -INFINITY && l_s[w * G + hh] == 0.f) continue;   // no token
       const float f = ex2(m_s[w * G + hh] - M);   // 0 for a warp that saw no token
       lsum += f * l_s[w * G + hh];
       const float4 x = *reinterpret_cast<const float4 *>(o_s + (w * G + hh) * D + d);
@@ -1012,13 +1056,56 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       a.z += f * x.z;
       a.w += f * x.w;
     }
-    if (kWalk != kWalkSuffix && nparts == 1) {
+    if constexpr (kWalk == kWalkSuffix) {
+      const size_t at = prefix_slot(p, g, 0) + static_cast<size_t>(b) * G + hh;
+      const size_t pitch = static_cast<size_t>(p.num_seqs) * G;
+      if (!joins) {
+        const size_t row = at + (p.slot0 + part) * pitch;
+        *reinterpret_cast<float4 *>(p.ws_o + row * D + d) = a;
+        if (d == 0) {
+          p.ws_m[row] = M;
+          p.ws_l[row] = lsum;
+        }
+        continue;
+      }
+      pdl_wait();   // the prefix's partials are visible from here on
+      const int na = prefix_partials<G>(p, group, b, hh);
+      const float M_own = M;
+      for (int k = 0; k < na; ++k) M = fmaxf(M, p.ws_m[at + k * pitch]);
+      const float f = M_own == -INFINITY && lsum == 0.f ? 0.f : ex2(M_own - M);
+      lsum *= f;
+      a.x *= f;
+      a.y *= f;
+      a.z *= f;
+      a.w *= f;
+      for (int k0 = 0; k0 < na; k0 += kJoinBatch) {
+        float mk[kJoinBatch], lk[kJoinBatch];
+        float4 x[kJoinBatch];
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u) {   // every load of the batch in flight
+          const size_t row = at + min(k0 + u, na - 1) * pitch;
+          mk[u] = p.ws_m[row];
+          lk[u] = k0 + u < na ? p.ws_l[row] : 0.f;
+          x[u] = *reinterpret_cast<const float4 *>(p.ws_o + row * D + d);
+        }
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u) {
+          if (k0 + u >= na || (mk[u] == -INFINITY && lk[u] == 0.f)) continue;   // no token: o may be anything
+          const float fk = ex2(mk[u] - M);
+          lsum += fk * lk[u];
+          a.x += fk * x[u].x;
+          a.y += fk * x[u].y;
+          a.z += fk * x[u].z;
+          a.w += fk * x[u].w;
+        }
+      }
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;   // no token at all: zeros
+      Elem<T>::store4(out + i, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    } else if (nparts == 1) {
       const float inv = kWalk == kWalkSelected && lsum == 0.f ? 0.f : 1.f / lsum;   // an empty list: zeros
       Elem<T>::store4(out + i, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     } else {
-      size_t row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.max_partitions + part;
-      if constexpr (kWalk == kWalkSuffix)
-        row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.slots + p.slot0 + part;
+      const size_t row = (static_cast<size_t>(b) * p.num_heads + h0 + hh) * p.max_partitions + part;
       *reinterpret_cast<float4 *>(p.ws_o + row * D + d) = a;
       if (d == 0) {
         p.ws_m[row] = M;
@@ -1149,20 +1236,21 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_decode_reduce_kernel(con
 
 // Combine the partials of the shared-prefix and selected-block walks: a warp per
 // (sequence, query head) row, the same sums as pa_decode_reduce_kernel.  A row has
-// `slots` partials in the workspace, of which two runs are used: the first na
-// and nb from slot0 on.  A partial with m = -inf and l = 0 holds no token and its o
+// partials in the workspace at row `at` of each slot, slots `pitch` rows apart, of
+// which two runs are used: the first na and nb from slot0 on.  A partial with m = -inf and l = 0 holds no token and its o
 // is not used; a row without any token is zeros.
 template <typename T, typename Params>
-__device__ __forceinline__ void join_row(const Params &p, long long row, int slots, int na, int slot0, int nb) {
+__device__ __forceinline__ void join_row(const Params &p, long long row, size_t at, size_t pitch, int na, int slot0, int nb) {
   constexpr int D = kChunksPerRow * Elem<T>::kPerChunk;
   constexpr int PER_LANE = D / 32;
   const int lane = threadIdx.x & 31;
-  const float *m = p.ws_m + row * slots;
-  const float *l = p.ws_l + row * slots;
-  const float *o = p.ws_o + row * slots * D + lane * PER_LANE;
+  const float *m = p.ws_m + at;
+  const float *l = p.ws_l + at;
+  const float *o = p.ws_o + at * D + lane * PER_LANE;
+  auto slot = [&](int i) { return static_cast<size_t>(i < na ? i : slot0 + i - na) * pitch; };
   const int n = na + nb;
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, m[i < na ? i : slot0 + i - na]);
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, m[slot(i)]);
   M = warp_max(M);
   float lsum = 0.f;
   float acc[PER_LANE];
@@ -1171,16 +1259,15 @@ __device__ __forceinline__ void join_row(const Params &p, long long row, int slo
   for (int i0 = 0; i0 < n; i0 += kReduceBatch) {
     const int iu = i0 + lane % kReduceBatch;
     const bool live = lane < kReduceBatch && iu < n;
-    const int su = iu < na ? iu : slot0 + iu - na;
-    const float m_u = live ? m[su] : -INFINITY;
-    const float l_u = live ? l[su] : 0.f;
+    const float m_u = live ? m[slot(iu)] : -INFINITY;
+    const float l_u = live ? l[slot(iu)] : 0.f;
     float w[kReduceBatch], li[kReduceBatch], x[kReduceBatch][PER_LANE];
 #pragma unroll
     for (int u = 0; u < kReduceBatch; ++u) {   // every load of the batch in flight
       const int i = min(i0 + u, n - 1);
       w[u] = __shfl_sync(kFullMask, m_u, u);
       li[u] = __shfl_sync(kFullMask, l_u, u);
-      const float *src = o + static_cast<size_t>(i < na ? i : slot0 + i - na) * D;
+      const float *src = o + slot(i) * D;
       if constexpr (PER_LANE == 4) {
         const float4 v = *reinterpret_cast<const float4 *>(src);
         x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
@@ -1216,7 +1303,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_join_selected_kernel(con
   for (long long row = static_cast<long long>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5); row < rows; row += step) {
     const int L = p.context_lens[row / p.num_heads];
     if (L <= 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize) continue;   // as the partition kernel
-    join_row<T>(p, row, p.max_partitions, p.max_partitions, 0, 0);
+    join_row<T>(p, row, row * p.max_partitions, 1, p.max_partitions, 0, 0);
   }
 }
 

@@ -45,7 +45,6 @@
 
 namespace pa {
 
-constexpr int kPrefixRows = 128;
 constexpr int kPrefixKv = 128;            // tokens of a K/V tile
 constexpr int kPrefixThreads = 384;
 constexpr int kPrefixMmaWarp = 8;
@@ -54,7 +53,6 @@ constexpr int kPrefixStagesPair = 5;      // one ring
 constexpr int kPrefixStagesSplit = 3;     // each of two rings
 
 struct PrefixParams : SuffixParams {
-  int parts, part_tokens;   // partitions of the longest prefix; tokens of each (a multiple of 128)
   int row_ctas;             // CTAs of 256 rows a (group, KV head, partition)
 };
 
@@ -63,21 +61,101 @@ struct PrefixSmem {
   static constexpr int kHalf = 128 * 128;
   static constexpr int kTiles = 7;                         // pair: 2 Q + 5 stages; split: 1 Q + 2 x 3 stages
   static constexpr int kBar = kTiles * kTile;
-  // full[6], free[6]; per w: s_full, p_half, p_full, o_done; drain
-  static constexpr int kNumBars = 12 + 8 + 1;
+  // full[6], free[6]; per w: s_full, p_half, p_full, o_done; drain; turn[2]
+  static constexpr int kNumBars = 12 + 8 + 3;
   static constexpr int kTmemSlot = kBar + 8 * kNumBars;
   static constexpr int kFlag = kTmemSlot + 4;
   static constexpr int kBytes = kFlag + 4;
   static constexpr int kAlloc = kBytes + 1024;             // + alignment of the base to 1024 B (swizzle atoms)
 };
 static_assert(PrefixSmem::kAlloc <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+static_assert(2 * kPrefixRows * 512 <= PrefixSmem::kBar, "staged rows");
 static_assert(2 + kPrefixStagesPair <= PrefixSmem::kTiles && 1 + 2 * kPrefixStagesSplit <= PrefixSmem::kTiles, "tiles");
 
-// How many partials of the prefix a row has, from its place in the group: the
-// CTAs of its 256 rows run as "split" (two a partition) if the group has at most
-// 128 rows from the CTA's first on, else as "pair" (one).
-__device__ __forceinline__ bool prefix_split(int rows_in_group, int row_cta) {
-  return rows_in_group - row_cta * 2 * kPrefixRows <= kPrefixRows;
+// Bounded wait of the hand-overs between roles.  The timer is first read after 32
+// polls: reading %globaltimer costs hundreds of cycles, which a wait that is
+// about to end must not pay.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort_flag,
+                                          unsigned long long limit_ns) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort_flag || now - t0 > limit_ns) return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// 16 consecutive 32-bit columns of this thread's lane from raw words.
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// AND of `pred` over the 256 softmax threads (named barrier 1).
+__device__ __forceinline__ bool softmax_all(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred p, 1, 256, p;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+
+// Largest of N consecutive scores (N a multiple of 16).
+template <int N>
+__device__ __forceinline__ float row_max(const float *s) {
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx[k] = fmaxf(s[k], s[8 + k]);
+#pragma unroll
+  for (int c = 16; c < N; c += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx[k] = max3(mx[k], s[c + k], s[c + 8 + k]);
+  return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+// P = 2^((s - m) c2) of 64 scores -> tensor memory at taddr: 32 columns of pairs (the
+// upper 16 bits as they are for bf16, rounded for fp16) and, for bf16, 32 columns
+// of what those leave, rounded.  Returns two partial sums of P.
+template <typename PK, bool kLo>
+__device__ __forceinline__ float2 exp_half(const float *s, float c2, float m, uint32_t taddr) {
+  const float2 nmc = make_float2(-m * c2, -m * c2);
+  const float2 cc2 = make_float2(c2, c2);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t hi[16], lo[kLo ? 16 : 1];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = __ffma2_rn(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), cc2, nmc);
+      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      sum[k & 1] = __fadd2_rn(sum[k & 1], e);
+      if constexpr (kLo) {
+        const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
+        hi[k] = __byte_perm(ux, uy, 0x7632);
+        lo[k] = PK::pack(e.x - __uint_as_float(ux & 0xffff0000u), e.y - __uint_as_float(uy & 0xffff0000u));
+      } else {
+        hi[k] = PK::pack(e.x, e.y);
+      }
+    }
+    tmem_st16u(taddr + 16 * q, hi);
+    if constexpr (kLo) tmem_st16u(taddr + 32 + 16 * q, lo);
+  }
+  return __fadd2_rn(sum[0], sum[1]);
 }
 
 template <typename T, int G>
@@ -95,6 +173,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   uint64_t *free_ = full + 6;
   uint64_t *tile_bars = free_ + 6;   // w: s_full, p_half, p_full, o_done at 4 w
   uint64_t *drain = tile_bars + 8;
+  uint64_t *turn = drain + 1;        // [w]: the other's PV that w's next one follows is issued
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kTmemSlot);
   volatile int *abort_s = reinterpret_cast<int *>(smem + SM::kFlag);
 
@@ -143,7 +222,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   auto ring_base = [&](int w) { return split ? w * kPrefixStagesSplit : 0; };
   auto stage_ptr = [&](int st) { return smem + (q_tiles + st) * SM::kTile; };
 
-  if (tid == 0) {
+  if (warp == kPrefixLoadWarp && lane == 0) {
     for (int i = 0; i < 6; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&free_[i], split ? 1 : 2);   // one arrival per consuming issuer
@@ -156,6 +235,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_init(&tb[3], 1);   // o_done
     }
     mbar_init(drain, 2);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
     fence_mbar_init();
     *abort_s = 0;
   }
@@ -163,6 +244,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  // ---- the first 32 block ids (TMA warps), in flight while Q is put in place
+  int my_id = static_cast<int>(p.num_blocks);   // past the end of the pool: the box reads zeros
+  auto load_ids = [&](int grp) {
+    const int lb = (grp << 5) + lane;
+    my_id = static_cast<int>(p.num_blocks);
+    if (lb < nblk) {
+      const int v = bt_row[lb];
+      if (v < 0 || v >= p.num_blocks) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, v);
+      else my_id = v;
+    }
+  };
+  if (warp >= kPrefixLoadWarp) load_ids(0);
   // ---- Q -> shared memory, K-major 128-byte swizzled: [d half][row][128 B]; warpgroup w its tile
   if (warp < kPrefixMmaWarp && (warp < 4 || !split)) {
     const int w = warp >> 2;
@@ -191,39 +284,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  int last_item[6];   // TMA warps: the last item issued into each stage of their ring (for the abort drain)
-#pragma unroll
-  for (int i = 0; i < 6; ++i) last_item[i] = -1;
-
+  int issued = 0;   // TMA warps: items taken (for the abort drain)
   if (warp >= kPrefixLoadWarp) {
     // ================================================================ TMA producers
     const int w = warp - kPrefixLoadWarp;
     if (w == 0 || split) {
       const int n = tiles_of(w);
       const int base = ring_base(w);
-      int grp = -1, my_id = 0;
+      int grp = 0;
       for (int it = 0; it < 2 * n; ++it) {   // item it: K (even) or V (odd) of this ring's tile it / 2
         const int st = it % ring_len;
         if (it >= ring_len &&
-            !__all_sync(kFullMask, mbar_wait_or_abort(&free_[base + st], (it / ring_len - 1) & 1, abort_s, wait_limit, true)))
+            !__all_sync(kFullMask, role_wait(&free_[base + st], (it / ring_len - 1) & 1, abort_s, wait_limit)))
           break;
         const int j = split ? 2 * (it >> 1) + w : it >> 1;
-        const int want = (8 * j) >> 5;
-        if (want != grp) {
-          grp = want;
-          const int lb = (grp << 5) + lane;
-          my_id = static_cast<int>(p.num_blocks);   // past the end of the pool: the box reads zeros
-          if (lb < nblk) {
-            const int v = bt_row[lb];
-            if (v < 0 || v >= p.num_blocks) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, v);
-            else my_id = v;
-          }
+        if (((8 * j) >> 5) != grp) {
+          grp = (8 * j) >> 5;
+          load_ids(grp);
         }
         int ids[8];
 #pragma unroll
         for (int bi = 0; bi < 8; ++bi) ids[bi] = __shfl_sync(kFullMask, my_id, (8 * j + bi) & 31);
-        const bool skip = stall_here && it == 0 && w == 0;   // test hook: K tile 0 left unissued
-        if (lane == 0 && !skip) {
+        if (lane == 0 && !(stall_here && it == 0 && w == 0)) {   // (test hook: K tile 0 left unissued)
           uint8_t *dst = stage_ptr(base + st);
           uint64_t *bar = &full[base + st];
           const CUtensorMap *tm = (it & 1) ? &tm_v : &tm_k;
@@ -234,18 +316,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             for (int half = 0; half < 2; ++half)
               tma_load_5d(dst + half * SM::kHalf + bi * (kBlockSize * 128), tm, 0, half, g, 0, ids[bi], bar);
         }
-        if (!skip) {
-#pragma unroll
-          for (int i = 0; i < 6; ++i)
-            if (i == st) last_item[i] = it;
-        }
+        issued = it + 1;
       }
     }
   } else if (warp >= kPrefixMmaWarp) {
     if (lane == 0) {
-      // ================================================================ tensor-core issue
+      // ================================================================ tensor-core issue for w
       const int w = warp - kPrefixMmaWarp;
-      const int n = tiles_of(w);
+      const int n = tiles_of(w), n_other = tiles_of(1 - w);
       const int base = ring_base(w);
       uint64_t *tb = tile_bars + 4 * w;
       constexpr uint32_t kIdescQK = instr_desc_f16(PK::kFormat, false, kPrefixRows, kPrefixKv);
@@ -253,48 +331,54 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
-        ok = mbar_test_wait(bar, parity) || mbar_wait_or_abort(bar, parity, abort_s, wait_limit);
+        ok = role_wait(bar, parity, abort_s, wait_limit);
         if (!ok) {
           record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
           *abort_s = 1;
         }
         tc_fence_after();
       };
-      const uint64_t a_qk = smem_desc_sw128(smem + (split ? 0 : w) * SM::kTile, 16, 1024);
+      // an operand at byte offset `off` from a tile's base has the base's descriptor
+      // with off / 16 added (the address field does not overflow: shared memory ends below 2^18)
+      const uint64_t a0 = smem_desc_sw128(smem + (split ? 0 : w) * SM::kTile, 16, 1024);
       const uint64_t k_desc = smem_desc_sw128(stage_ptr(base), 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(stage_ptr(base), SM::kHalf, 1024);
       const uint32_t s_tmem = tmem + w * 256, o_tmem = s_tmem + 128;
       for (int i = 0; i < n && ok; ++i) {
-        const int ik = 2 * i, iv = 2 * i + 1;
-        wait(&full[base + ik % ring_len], (ik / ring_len) & 1);
+        const int sk = (2 * i) % ring_len, sv = (2 * i + 1) % ring_len;
+        wait(&full[base + sk], (2 * i / ring_len) & 1);
         if (i > 0) wait(&tb[3], (i - 1) & 1);   // PV(i-1) has read P from S's columns
         if (!ok) break;
-        const uint64_t b0 = k_desc + (((ik % ring_len) * SM::kTile) >> 4);
+        const uint64_t b0 = k_desc + ((sk * SM::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16(s_tmem, a_qk + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4),
+          umma_f16(s_tmem, a0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4),
                    b0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
         umma_commit(&tb[0]);
-        umma_commit(&free_[base + ik % ring_len]);
-        wait(&full[base + iv % ring_len], (iv / ring_len) & 1);
+        wait(&full[base + sv], ((2 * i + 1) / ring_len) & 1);
+        if (i > 0 || w > 0) {   // PV_0(i) follows PV_1(i-1), PV_1(i) follows PV_0(i)
+          const int before = w > 0 ? i : i - 1;
+          if (before < n_other) wait(&turn[w], before & 1);
+        }
         if (!ok) break;
-        const uint64_t v0 = v_desc + (((iv % ring_len) * SM::kTile) >> 4);
+        const uint64_t v0 = v_desc + ((sv * SM::kTile) >> 4);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           wait(&tb[1 + hf], i & 1);   // the half's P written
           if (!ok) break;
 #pragma unroll
           for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {   // 16 tokens = 8 columns of P a step
-            umma_f16_ts(o_tmem, s_tmem + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdescPV, i > 0 || kk > 0);
-            if constexpr (kLo) umma_f16_ts(o_tmem, s_tmem + 64 + kk * 8, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
+            const uint32_t p_tmem = s_tmem + 64 * hf + (kk & 3) * 8;
+            umma_f16_ts(o_tmem, p_tmem, v0 + ((kk * 16 * 128) >> 4), kIdescPV, i > 0 || kk > 0);
+            if constexpr (kLo) umma_f16_ts(o_tmem, p_tmem + 32, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
           }
         }
         if (!ok) break;
         umma_commit(&tb[3]);
-        umma_commit(&free_[base + iv % ring_len]);
+        mbar_arrive(&turn[1 - w]);
       }
     }
-  } else {
+  } else if (warp < kPrefixMmaWarp) {
     // ================================================================ softmax warpgroup w
     const int w = warp >> 2;
     const int n = tiles_of(w);
@@ -309,16 +393,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (!ok) return;
-      ok = __all_sync(kFullMask, mbar_wait_or_abort(bar, parity, abort_s, wait_limit));
+      ok = __all_sync(kFullMask, role_wait(bar, parity, abort_s, wait_limit));
       if (!ok && lane == 0) {
         record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
         *abort_s = 1;
       }
       tc_fence_after();
     };
+    auto hand_over = [&](uint64_t *bar) {   // this warp's P is in tensor memory
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     for (int i = 0; i < n && ok; ++i) {
       wait(&tb[0], i & 1);
       if (!ok) break;
+      // QK(i) is complete, and so is PV(i-1), which it waited for: their stages are free
+      if ((tid & 127) == 0) {
+        const int base = ring_base(w);
+        mbar_arrive(&free_[base + 2 * i % ring_len]);
+        if (i > 0) mbar_arrive(&free_[base + (2 * i - 1) % ring_len]);
+      }
       float s[128];
       tmem_ld64(t_s, *reinterpret_cast<float (*)[64]>(s));
       tmem_ld64(t_s + 64, *reinterpret_cast<float (*)[64]>(s + 64));
@@ -327,79 +423,60 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = c < live ? s[c] : -INFINITY;
       }
-      float mx[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mx[k] = s[k];
-#pragma unroll
-      for (int c = 8; c < 128; ++c) mx[c & 7] = fmaxf(mx[c & 7], s[c]);
-      const float tmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-      bool need = false;
-      float f = 1.f;
-      if (i == 0) {
-        m_run = tmax;
-      } else if ((tmax - m_run) * c2 > kRescaleLog2) {
-        need = true;
-        f = ex2((m_run - tmax) * c2);
-        m_run = tmax;
-        l_run *= f;
-      }
-      if (__any_sync(kFullMask, need)) {   // PV(i-1) is complete: QK(i) was issued after it
+      if (i == 0) m_run = row_max<128>(s);
+      // m_run, the reference of the exponentials, follows only a score that passes it by more than 2^8
+      if (i > 0) {
+        const float tmax = row_max<128>(s);
+        const bool need = (tmax - m_run) * c2 > kRescaleLog2;
+        if (__any_sync(kFullMask, need)) {
+          // O, complete up to tile i-1 (QK(i) was issued after PV(i-1)), follows
+          const float f = need ? ex2((m_run - tmax) * c2) : 1.f;
+          if (need) m_run = tmax;
+          l_run *= f;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(t_o + c, o);
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= f;
-          tmem_st32(t_o + c, o);
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            tmem_st32(t_o + c, o);
+          }
         }
       }
-      const float2 nmc = make_float2(-m_run * c2, -m_run * c2);
-      const float2 cc2 = make_float2(c2, c2);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t hi[32], lo[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 x = __ffma2_rn(make_float2(s[64 * hf + 2 * k], s[64 * hf + 2 * k + 1]), cc2, nmc);
-          const float2 e = make_float2(ex2(x.x), ex2(x.y));
-          sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-          hi[k] = PK::pack(e.x, e.y);
-          if constexpr (kLo)
-            lo[k] = PK::pack(e.x - __uint_as_float(hi[k] << 16), e.y - __uint_as_float(hi[k] & 0xffff0000u));
-        }
-        tmem_st32u(t_s + 32 * hf, hi);
-        if constexpr (kLo) tmem_st32u(t_s + 64 + 32 * hf, lo);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tb[1 + hf]);
-      }
-      l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      float2 sum = exp_half<PK, kLo>(s, c2, m_run, t_s);
+      hand_over(&tb[1]);
+      sum = __fadd2_rn(sum, exp_half<PK, kLo>(s + 64, c2, m_run, t_s + 64));
+      hand_over(&tb[2]);
+      l_run += sum.x + sum.y;
     }
-    // ---- this row's partial: m in base-2 units, o and l relative to it
+    // ---- this warp's 32 rows of partials: m in base-2 units, o and l relative to it.  In
+    // the workspace they are consecutive, so o goes through shared memory (Q and the
+    // K/V stages, free once both warpgroups' products are complete; 16-byte chunk c
+    // of row r at c ^ (r & 31)) and out 512 consecutive bytes a warp store.  A thread
+    // storing its own row, or one bulk copy a row, took 14000 and 8000 cycles.
     if (n > 0) wait(&tb[3], (n - 1) & 1);
-    const int rg = row0 + (split ? 0 : w * kPrefixRows) + r;
-    if (ok && rg < rows_group) {
-      const size_t row = static_cast<size_t>(s0 + rg / G) * p.num_heads + g * G + rg % G;
-      const size_t slot = row * p.slots + (split ? 2 * part + w : part);
-      p.ws_m[slot] = n > 0 ? m_run * c2 : -INFINITY;
-      p.ws_l[slot] = l_run;
+    const int rw = row0 + (split ? 0 : w * kPrefixRows) + (r & ~31);   // the warp's first row
+    const size_t at = prefix_slot(p, g, split ? 2 * part + w : part) + static_cast<size_t>(s0) * G + rw;
+    if (ok && rw + lane < rows_group) {
+      p.ws_m[at + lane] = n > 0 ? m_run * c2 : -INFINITY;
+      p.ws_l[at + lane] = l_run;
     }
-    if (ok && n > 0) {
-      const bool stored = rg < rows_group;
-      const size_t row = static_cast<size_t>(s0 + (stored ? rg / G : 0)) * p.num_heads + g * G + rg % G;
-      float *dst = p.ws_o + (row * p.slots + (split ? 2 * part + w : part)) * D;
+    if (softmax_all(ok) && n > 0) {
+      uint8_t *stage = smem + (warp * 32) * 512;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(t_o + c, o);
-        if (stored) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4 *>(dst + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
+        for (int k = 0; k < 32; k += 4)
+          *reinterpret_cast<float4 *>(stage + lane * 512 + ((((c + k) >> 2) ^ lane) << 4)) =
+              make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
       }
+      __syncwarp();
+      float4 *dst = reinterpret_cast<float4 *>(p.ws_o) + at * (D / 4) + lane;
+      const int rows = min(32, rows_group - rw);
+#pragma unroll 8
+      for (int k = 0; k < rows; ++k) dst[k * (D / 4)] = *reinterpret_cast<const float4 *>(stage + k * 512 + ((lane ^ k) << 4));
     }
     tc_fence_before();
   }
@@ -412,10 +489,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     mbar_wait(drain, 0, wait_limit);
   }
   if (*abort_s && warp >= kPrefixLoadWarp && lane == 0) {
-    const int base = ring_base(warp - kPrefixLoadWarp);
-#pragma unroll
-    for (int i = 0; i < 6; ++i)
-      if (last_item[i] >= 0) mbar_wait(&full[base + i], (last_item[i] / ring_len) & 1, wait_limit);
+    // the last item issued into each stage (an earlier one's copy landed before its stage was reissued)
+    const int w = warp - kPrefixLoadWarp;
+    for (int it = max(0, issued - ring_len); it < issued; ++it)
+      if (!(stall_here && it == 0 && w == 0)) mbar_wait(&full[ring_base(w) + it % ring_len], (it / ring_len) & 1, wait_limit);
   }
   __syncthreads();
   if (warp == kPrefixMmaWarp) {
@@ -424,7 +501,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
 }
 
-// Join of a row's prefix partials (slots 0 ..) and those of its own tokens (slot0 ..).
+// Join of a row's prefix partials (slots 0 ..) and those of its own tokens (slot0 ..):
+// only where the own tokens are more than one partition (else the suffix walk does it).
 template <typename T, int G>
 __global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const PrefixParams p) {
   pdl_wait();
@@ -433,15 +511,14 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const
   const long long step = static_cast<long long>(gridDim.x) * kReduceWarps;
   for (long long row = static_cast<long long>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5); row < rows; row += step) {
     const int b = static_cast<int>(row / p.num_heads);
+    const int h = static_cast<int>(row % p.num_heads);
     const int L = p.context_lens[b];
     const PrefixGroup group = group_of(p, b);
     if (!group.ok || L < group.prefix || L - group.prefix > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize)
       continue;   // recorded by the partition kernel; the row is left as it was
-    const int rows_group = (group.s1 - group.s0) * G;
-    const int rg = (b - group.s0) * G + static_cast<int>(row % p.num_heads) % G;
-    const int parts = (group.prefix + p.part_tokens - 1) / p.part_tokens;
-    const int na = prefix_split(rows_group, rg / (2 * kPrefixRows)) ? 2 * parts : parts;
-    join_row<T>(p, row, p.slots, na, p.slot0, (L - group.prefix + p.partition_size - 1) / p.partition_size);
+    join_row<T>(p, row, prefix_slot(p, h / G, 0) + static_cast<size_t>(b) * G + h % G,
+                static_cast<size_t>(p.num_seqs) * G, prefix_partials<G>(p, group, b, h % G), p.slot0,
+                (L - group.prefix + p.partition_size - 1) / p.partition_size);
   }
 }
 
