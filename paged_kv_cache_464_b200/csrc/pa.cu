@@ -680,19 +680,24 @@ bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Heads a thread: three where that leaves a wave of CTAs (256 threads, up to eight an
+// SM), one below that, where the number of CTAs counts more.
 template <typename T>
 pa_status_t launch_rope(const pa::RopeParams &p, bool interleaved, bool fp8, cudaStream_t stream) {
-  const int H = p.num_heads + 2 * p.num_kv_heads;
-  const int HS = (H + p.heads_per_thread - 1) / p.heads_per_thread;
-  const long long total = (long long)p.num_tokens * HS * (pa::kChunksPerRow / 2);
-  long long ctas = (total + 255) / 256;
-  if (ctas > 64LL * sm_count()) ctas = 64LL * sm_count();
-  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)ctas), dim3(256), 0, stream, p); };
+  const int rows = p.num_heads + 2 * p.num_kv_heads;
+  const unsigned tokens = (unsigned)((p.num_tokens + pa::kRopeTokens - 1) / pa::kRopeTokens);
+  const bool many = (long long)tokens * ((rows + 23) / 24) >= 8LL * sm_count();
+  const int per_cta = pa::kRopeHeads * (many ? 3 : 1);
+  const dim3 grid(tokens, (unsigned)((rows + per_cta - 1) / per_cta));
+  auto go = [&](auto kernel) { return launch(kernel, grid, dim3(256), 0, stream, p); };
+  auto pick = [&](auto inter, auto quant) {
+    constexpr bool I = decltype(inter)::value, Q = decltype(quant)::value;
+    return many ? go(pa::rope_and_cache_kernel<T, I, Q, 3>) : go(pa::rope_and_cache_kernel<T, I, Q, 1>);
+  };
   if constexpr (!std::is_same<T, float>::value) {
-    if (fp8)
-      return interleaved ? go(pa::rope_and_cache_kernel<T, true, true>) : go(pa::rope_and_cache_kernel<T, false, true>);
+    if (fp8) return interleaved ? pick(std::true_type{}, std::true_type{}) : pick(std::false_type{}, std::true_type{});
   }
-  return interleaved ? go(pa::rope_and_cache_kernel<T, true, false>) : go(pa::rope_and_cache_kernel<T, false, false>);
+  return interleaved ? pick(std::true_type{}, std::false_type{}) : pick(std::false_type{}, std::false_type{});
 }
 
 // cache_dtype: dtype, or PA_FP8_E4M3.
@@ -746,7 +751,6 @@ pa_status_t rope_impl(void *q_out, const void *q, const void *key, const void *v
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.rotary = rotary_dim;
-  p.heads_per_thread = 1;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   const bool fp8 = cache_dtype == PA_FP8_E4M3;
@@ -801,8 +805,9 @@ struct PrefixPlan {
   WorkspaceLayout ws;
 };
 
-// Partitions: as many as give the shortest run, a wave of one CTA an SM taking
-// the tiles of its longest partition plus about three tiles' time of set-up and epilogue.
+// Partitions: as many as give the shortest run, in units of half a tile's time: a
+// wave of one CTA an SM takes the tiles of its longest partition plus about five
+// tiles' time of set-up and epilogue, and each partition adds a partial to combine.
 PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_prefix_len,
                        int max_suffix_len, int max_group_size) {
   PrefixPlan r{};
@@ -818,7 +823,7 @@ PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_h
     for (int parts = 1; parts <= tiles && parts <= 64; ++parts) {
       const int t = (tiles + parts - 1) / parts;
       const long long waves = (ctas * parts + sms - 1) / sms;
-      const long long cost = waves * (t + 3);
+      const long long cost = waves * (2 * t + 10) + parts;
       if (cost < best) {
         best = cost;
         per = t;
@@ -1019,16 +1024,26 @@ pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, cons
 
 namespace {
 
+template <typename T, int G>
+pa_status_t launch_choice(const pa::SelectParams &p, cudaStream_t s) {
+  if (p.max_blocks > p.num_selected) {   // else no sequence has more blocks than are chosen
+    const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.chunks;
+    if (grid > INT32_MAX) return PA_ERR_SHAPE;
+    const pa_status_t st =
+        launch(pa::block_score_kernel<T, G>, dim3((unsigned)grid), dim3(pa::kScoreWarps * 32), 0, s, p);
+    if (st != PA_OK) return st;
+  }
+  return launch(pa::block_select_kernel<T, G>, dim3((unsigned)(p.num_seqs * p.num_kv_heads)),
+                dim3(pa::kSelectThreads), 0, s, p);
+}
+
 template <typename T>
-pa_status_t launch_scores(int group, const pa::SelectParams &p, cudaStream_t s) {
-  const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.chunks;
-  if (grid > INT32_MAX) return PA_ERR_SHAPE;
-  auto go = [&](auto kernel) { return launch(kernel, dim3((unsigned)grid), dim3(pa::kScoreWarps * 32), 0, s, p); };
+pa_status_t dispatch_choice(int group, const pa::SelectParams &p, cudaStream_t s) {
   switch (group) {
-    case 1: return go(pa::block_score_kernel<T, 1>);
-    case 2: return go(pa::block_score_kernel<T, 2>);
-    case 4: return go(pa::block_score_kernel<T, 4>);
-    case 8: return go(pa::block_score_kernel<T, 8>);
+    case 1: return launch_choice<T, 1>(p, s);
+    case 2: return launch_choice<T, 2>(p, s);
+    case 4: return launch_choice<T, 4>(p, s);
+    case 8: return launch_choice<T, 8>(p, s);
   }
   return PA_ERR_SHAPE;
 }
@@ -1040,7 +1055,7 @@ extern "C" {
 size_t pa_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_context_len) {
   if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len <= 0) return 0;
   const size_t blocks = ((size_t)max_context_len + kBlockSize - 1) / kBlockSize;
-  return align256((size_t)num_seqs * num_kv_heads * blocks * sizeof(unsigned long long));
+  return 2 * align256((size_t)num_seqs * num_kv_heads * blocks * 8);   // fp32 scores with bounds, fp64 scores
 }
 
 pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block_bounds, const int32_t *block_tables,
@@ -1074,7 +1089,8 @@ pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block
   p.bounds = (const uint4 *)block_bounds;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
-  p.keys = (unsigned long long *)workspace;
+  p.approx = (float2 *)workspace;
+  p.keys = (unsigned long long *)(static_cast<char *>(workspace) + need / 2);
   p.selected = selected;
   p.num_blocks = num_blocks;
   p.num_seqs = num_seqs;
@@ -1088,16 +1104,13 @@ pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block
   p.recent = recent_blocks;
   p.chunks = (p.max_blocks + pa::kScoreBlocks - 1) / pa::kScoreBlocks;
   cudaStream_t s = (cudaStream_t)stream;
-  if (p.max_blocks > num_selected) {   // else no sequence has more blocks than are chosen
-    switch (dtype) {
-      case PA_F32: st = launch_scores<float>(group, p, s); break;
-      case PA_F16: st = launch_scores<__half>(group, p, s); break;
-      case PA_BF16: st = launch_scores<__nv_bfloat16>(group, p, s); break;
-      case PA_FP8_E4M3: return PA_ERR_DTYPE;
-    }
-    if (st != PA_OK) return st;
+  switch (dtype) {
+    case PA_F32: return dispatch_choice<float>(group, p, s);
+    case PA_F16: return dispatch_choice<__half>(group, p, s);
+    case PA_BF16: return dispatch_choice<__nv_bfloat16>(group, p, s);
+    case PA_FP8_E4M3: break;
   }
-  return launch(pa::block_select_kernel, dim3((unsigned)(num_seqs * num_kv_heads)), dim3(pa::kSelectThreads), 0, s, p);
+  return PA_ERR_DTYPE;
 }
 
 }  // extern "C"

@@ -102,7 +102,7 @@ struct DecodeParams {
 //   kWalkSelected  the tokens of the blocks that a list names, one list for each
 //                  (sequence, KV head) (pa_decode_selected)
 constexpr int kWalkAll = 0, kWalkSuffix = 1, kWalkSelected = 2;
-constexpr int kJoinBatch = 4;   // kWalkSuffix: the prefix's partials in flight per thread when it combines
+constexpr int kJoinBatch = 8;   // kWalkSuffix: the prefix's partials in flight per thread when it combines
 
 struct SuffixParams : DecodeParams {   // context_lens: whole lengths; max_context_len: of the suffix
   const int32_t *group_start;     // [num_groups + 1]

@@ -46,7 +46,7 @@ struct RopeParams {
   const int64_t *slot_mapping;      // [T]
   long long q_out_stride, q_stride, k_stride, v_stride;   // in elements
   long long num_slots, max_position;
-  int num_tokens, num_heads, num_kv_heads, rotary, heads_per_thread;
+  int num_tokens, num_heads, num_kv_heads, rotary;
   float k_scale, v_scale;           // 1-byte caches
 };
 
@@ -90,105 +90,115 @@ __device__ __forceinline__ uint2 pack_e4m3(const float *f, float scale) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// A head row is C = 16 chunks of 16 bytes, and an item of work is two of them:
-// the two halves of a rotated pair (item c: chunks c and c + r/2 in chunks), two
-// adjacent chunks of the interleaved form, or two adjacent chunks past r.  Each
-// head has C/2 = 8 items, so a warp covers four heads and its two loads four
-// 128-byte lines each.  A thread keeps its item's cosines and sines (2 * EPC fp32) in
-// registers for all the heads it takes (hs, hs + HS, ... of the token's Hq + 2
-// Hkv rows), which makes them a small part of what it loads.
-template <typename T, bool kInterleaved, bool kFp8>
-__global__ void __launch_bounds__(256) rope_and_cache_kernel(const RopeParams p) {
+// A head row is 16 chunks of 16 bytes, and an item of work is two of them: the
+// two halves of a rotated pair (item c: chunks c and c + r/2 in chunks), two adjacent
+// chunks of the interleaved form, or two adjacent chunks past r.  A CTA is 4 tokens x 8
+// heads x 8 items, so a warp covers four heads of a token and its two loads four
+// 128-byte lines each; a thread takes its item of NH heads, 8 apart, with every load in
+// flight before the first use (they do not wait for the position) and its
+// cosines and sines (2 * EPC fp32) in registers for all of them.
+constexpr int kRopeTokens = 4, kRopeHeads = 8, kRopeItems = kChunksPerRow / 2;
+
+template <typename T, bool kInterleaved, bool kFp8, int NH>
+__global__ void __launch_bounds__(kRopeTokens * kRopeHeads * kRopeItems) rope_and_cache_kernel(const RopeParams p) {
   constexpr int EPC = Elem<T>::kPerChunk;
-  constexpr int kItems = kChunksPerRow / 2;
   pdl_wait();
   pdl_trigger();
-  const int H = p.num_heads + 2 * p.num_kv_heads;
-  const int HS = (H + p.heads_per_thread - 1) / p.heads_per_thread;
-  const int per_token = HS * kItems;
+  const int c = threadIdx.x % kRopeItems;
+  const int tok = blockIdx.x * kRopeTokens + threadIdx.x / (kRopeItems * kRopeHeads);
+  if (tok >= p.num_tokens) return;
+  const int h0 = blockIdx.y * (kRopeHeads * NH) + threadIdx.x / kRopeItems % kRopeHeads;
+  const int n_rows = p.num_heads + 2 * p.num_kv_heads;   // the token's q, K and V rows
+  const long long pos = p.positions[tok];
+  const long long slot = p.slot_mapping[tok];
   const int rc = p.rotary / (2 * EPC);   // items that rotate
-  const long long total = static_cast<long long>(p.num_tokens) * per_token;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long k = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; k < total; k += stride) {
-    const int tok = static_cast<int>(k / per_token);
-    const int sub = static_cast<int>(k - static_cast<long long>(tok) * per_token);
-    const int c = sub % kItems, hs = sub / kItems;
-    const long long pos = p.positions[tok];
-    const long long slot = p.slot_mapping[tok];
-    if (pos < 0) continue;   // padding token: nothing is read or written
-    if (pos >= p.max_position) {
-      if (sub == 0) record_error(7 /*PA_DEV_BAD_POSITION*/, pos);
-      continue;
-    }
-    if (slot >= p.num_slots && sub == 0) record_error(2 /*PA_DEV_BAD_SLOT*/, slot);
-    const bool cached = slot >= 0 && slot < p.num_slots;
-    const bool turns = c < rc;
-    // the item's two chunks of a row
-    const int c0 = kInterleaved || !turns ? 2 * c : c;
-    const int c1 = kInterleaved || !turns ? 2 * c + 1 : c + rc;
-    float cs[EPC], sn[EPC];
-    if (turns) {
-      const float *row = p.cos_sin + pos * p.rotary + c * EPC;
+  const bool turns = c < rc;
+  // the item's two chunks of a row
+  const int c0 = kInterleaved || !turns ? 2 * c : c;
+  const int c1 = kInterleaved || !turns ? 2 * c + 1 : c + rc;
+  uint4 x0[NH], x1[NH];
 #pragma unroll
-      for (int e = 0; e < EPC; e += 4) {
-        *reinterpret_cast<float4 *>(cs + e) = *reinterpret_cast<const float4 *>(row + e);
-        *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(row + p.rotary / 2 + e);
-      }
-    }
-    for (int h = hs; h < H; h += HS) {
+  for (int u = 0; u < NH; ++u) {
+    const int h = h0 + u * kRopeHeads;
+    x0[u] = x1[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < n_rows) {
       const bool is_q = h < p.num_heads;
-      const bool is_k = !is_q && h < p.num_heads + p.num_kv_heads;
-      const int hl = is_q ? h : h - p.num_heads - (is_k ? 0 : p.num_kv_heads);
-      if (!is_q && !cached) continue;
-      const T *base = is_q ? static_cast<const T *>(p.q) + tok * p.q_stride
-                           : (is_k ? static_cast<const T *>(p.key) + tok * p.k_stride
-                                   : static_cast<const T *>(p.value) + tok * p.v_stride);
+      const bool is_k = h < p.num_heads + p.num_kv_heads;
+      const int hl = h - (is_q ? 0 : is_k ? p.num_heads : p.num_heads + p.num_kv_heads);
+      const T *base = static_cast<const T *>(is_q ? p.q : is_k ? p.key : p.value) +
+                      tok * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride);
       const uint4 *src = reinterpret_cast<const uint4 *>(base) + hl * kChunksPerRow;
-      uint4 x0 = src[c0], x1 = src[c1];
-      const bool rotate = turns && (is_q || is_k);
-      float f0[EPC], f1[EPC];
-      if (rotate || (kFp8 && !is_q)) {
-        Elem<T>::unpack(x0, f0);
-        Elem<T>::unpack(x1, f1);
-      }
-      if (rotate) {
-        if constexpr (kInterleaved) {
+      x0[u] = src[c0];
+      x1[u] = src[c1];
+    }
+  }
+  if (pos < 0) return;   // padding token: nothing is written
+  const bool first = threadIdx.x % (kRopeItems * kRopeHeads) == 0 && blockIdx.y == 0;
+  if (pos >= p.max_position) {
+    if (first) record_error(7 /*PA_DEV_BAD_POSITION*/, pos);
+    return;
+  }
+  if (slot >= p.num_slots && first) record_error(2 /*PA_DEV_BAD_SLOT*/, slot);
+  const bool cached = slot >= 0 && slot < p.num_slots;
+  float cs[EPC], sn[EPC];
+  if (turns) {
+    const float *row = p.cos_sin + pos * p.rotary + c * EPC;
 #pragma unroll
-          for (int e = 0; e < EPC; e += 2) {   // chunk 0 holds pairs 0 .. EPC/2 - 1 of the item, chunk 1 the rest
-            const float a0 = f0[e], b0 = f0[e + 1], a1 = f1[e], b1 = f1[e + 1];
-            const float g0 = cs[e / 2], s0 = sn[e / 2], g1 = cs[EPC / 2 + e / 2], s1 = sn[EPC / 2 + e / 2];
-            f0[e] = __fsub_rn(__fmul_rn(a0, g0), __fmul_rn(b0, s0));
-            f0[e + 1] = __fadd_rn(__fmul_rn(b0, g0), __fmul_rn(a0, s0));
-            f1[e] = __fsub_rn(__fmul_rn(a1, g1), __fmul_rn(b1, s1));
-            f1[e + 1] = __fadd_rn(__fmul_rn(b1, g1), __fmul_rn(a1, s1));
-          }
-        } else {
+    for (int e = 0; e < EPC; e += 4) {
+      *reinterpret_cast<float4 *>(cs + e) = *reinterpret_cast<const float4 *>(row + e);
+      *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(row + p.rotary / 2 + e);
+    }
+  }
 #pragma unroll
-          for (int e = 0; e < EPC; ++e) {
-            const float a = f0[e], b = f1[e];
-            f0[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-            f1[e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
-          }
+  for (int u = 0; u < NH; ++u) {
+    const int h = h0 + u * kRopeHeads;
+    const bool is_q = h < p.num_heads;
+    const bool is_k = !is_q && h < p.num_heads + p.num_kv_heads;
+    const int hl = h - (is_q ? 0 : is_k ? p.num_heads : p.num_heads + p.num_kv_heads);
+    if (h >= n_rows || (!is_q && !cached)) continue;
+    const bool rotate = turns && (is_q || is_k);
+    float f0[EPC], f1[EPC];
+    if (rotate || (kFp8 && !is_q)) {
+      Elem<T>::unpack(x0[u], f0);
+      Elem<T>::unpack(x1[u], f1);
+    }
+    if (rotate) {
+      if constexpr (kInterleaved) {
+#pragma unroll
+        for (int e = 0; e < EPC; e += 2) {   // chunk 0 holds pairs 0 .. EPC/2 - 1 of the item, chunk 1 the rest
+          const float a0 = f0[e], b0 = f0[e + 1], a1 = f1[e], b1 = f1[e + 1];
+          const float g0 = cs[e / 2], s0 = sn[e / 2], g1 = cs[EPC / 2 + e / 2], s1 = sn[EPC / 2 + e / 2];
+          f0[e] = __fsub_rn(__fmul_rn(a0, g0), __fmul_rn(b0, s0));
+          f0[e + 1] = __fadd_rn(__fmul_rn(b0, g0), __fmul_rn(a0, s0));
+          f1[e] = __fsub_rn(__fmul_rn(a1, g1), __fmul_rn(b1, s1));
+          f1[e + 1] = __fadd_rn(__fmul_rn(b1, g1), __fmul_rn(a1, s1));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          const float a = f0[e], b = f1[e];
+          f0[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+          f1[e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
         }
       }
-      if (kFp8 && !is_q) {
-        const float scale = is_k ? p.k_scale : p.v_scale;
-        uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) +
-                     (slot * p.num_kv_heads + hl) * kChunksPerRow;
-        dst[c0] = pack_e4m3(f0, scale);
-        dst[c1] = pack_e4m3(f1, scale);
-        continue;
-      }
-      if (rotate) {
-        x0 = pack_chunk<T>(f0);
-        x1 = pack_chunk<T>(f1);
-      }
-      uint4 *dst = is_q ? reinterpret_cast<uint4 *>(static_cast<T *>(p.q_out) + tok * p.q_out_stride) + hl * kChunksPerRow
-                        : reinterpret_cast<uint4 *>(is_k ? p.k_cache : p.v_cache) +
-                              (slot * p.num_kv_heads + hl) * kChunksPerRow;
-      dst[c0] = x0;
-      dst[c1] = x1;
     }
+    if (kFp8 && !is_q) {
+      const float scale = is_k ? p.k_scale : p.v_scale;
+      uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) +
+                   (slot * p.num_kv_heads + hl) * kChunksPerRow;
+      dst[c0] = pack_e4m3(f0, scale);
+      dst[c1] = pack_e4m3(f1, scale);
+      continue;
+    }
+    if (rotate) {
+      x0[u] = pack_chunk<T>(f0);
+      x1[u] = pack_chunk<T>(f1);
+    }
+    uint4 *dst = is_q ? reinterpret_cast<uint4 *>(static_cast<T *>(p.q_out) + tok * p.q_out_stride) + hl * kChunksPerRow
+                      : reinterpret_cast<uint4 *>(is_k ? p.k_cache : p.v_cache) +
+                            (slot * p.num_kv_heads + hl) * kChunksPerRow;
+    dst[c0] = x0[u];
+    dst[c1] = x1[u];
   }
 }
 

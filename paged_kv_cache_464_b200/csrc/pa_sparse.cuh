@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "pa_common.cuh"
+#include "pa_decode.cuh"
 
 namespace pa {
 
@@ -100,12 +101,18 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 }
 
 // ---------------------------------------------------------------- scores
+// Which blocks are chosen is decided by fp64 scores, but few of them are computed:
+// block_score_kernel gives every block an fp32 score with a bound on its error, and
+// block_select_kernel computes fp64 scores only for the blocks that the bound leaves in
+// doubt.  fp64 scores of all blocks cost 80 us for 8 x 8 x 2048 blocks and 8 heads
+// (two conversions to fp64 for each product, 16 a cycle and SM), against NEWSCORE.
 struct SelectParams {
   const void *q;                  // [S][Hq][D]
   const uint4 *bounds;            // [NB][2][Hkv][16 chunks]
   const int32_t *block_tables;    // [S][MBS]
   const int32_t *context_lens;    // [S]
-  unsigned long long *keys;       // [S][Hkv][max_blocks] scores in an order-preserving code
+  float2 *approx;                 // [S][Hkv][max_blocks] (score, error bound; not finite: in doubt)
+  unsigned long long *keys;       // [S][Hkv][max_blocks] fp64 scores in an order-preserving code
   int32_t *selected;              // [S][Hkv][K]
   long long num_blocks;
   int num_seqs, num_heads, num_kv_heads, max_blocks_per_seq, max_context_len;
@@ -114,8 +121,7 @@ struct SelectParams {
   int chunks;                     // CTAs a (sequence, KV head) in the score launch
 };
 
-// Doubles as unsigned integers in the same order (-0 below +0, which add up
-// equal only by a sum of all zeros: both are then mapped to +0); NaN is largest.
+// Doubles as unsigned integers in the same order (-0 as +0); NaN is largest.
 __device__ __forceinline__ unsigned long long score_key(double s) {
   if (s != s) return ~0ull;
   const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(s + 0.0));
@@ -123,15 +129,136 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
 }
 
 constexpr int kScoreWarps = 4;
-constexpr int kScoreBlocks = 64;   // blocks a CTA scores: 8 for each of its 8 half warps
+constexpr int kScoreBlocks = 64;   // blocks a CTA scores: 16 a warp
+// |fp32 score - score| <= kScoreError * sum_d |q_d| max(|lo_d|, |hi_d|).  The products of
+// 16-bit values are exact; a sum of 256 of them in fp32, whatever its order and if each
+// step drops bits below 2^-23 of the larger operand, is off by less than 2^-15 of
+// the sum of magnitudes; 64 fp32 products and sums by less than 2^-17.
+constexpr float kScoreError = 1.f / 16384;
 
-// A half warp scores a block: lane c of it holds chunk c of the block's two
-// rows and of the G query rows.  Sums are fp64 (the products of 16-bit values
-// are exact in fp32, those of fp32 values in fp64), so that the order in which
-// terms are added decides no near tie.
+// 16-bit caches: s_h(j) = q+ . hi + q- . lo with q+ = max(q, 0), q- = min(q, 0), as
+// warp-level matrix products (m16n8k16): 16 blocks by 8 heads, head_dim in any
+// order as long as both operands agree -- so each lane loads 16-byte chunks (eight
+// elements, the k slots of two products) of its rows straight from global memory, 256
+// bytes a lane in flight.  A third product gives the error bound's sum.
+template <typename T, int G>
+__device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, int j0, int n) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  uint4 qv[4];   // head gid: elements 32 i + 8 tig ..
+  const uint4 *qg = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q)) +
+                    (static_cast<size_t>(b) * p.num_heads + g * G) * kChunksPerRow;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) qv[i] = gid < G ? qg[gid * kChunksPerRow + 4 * i + tig] : make_uint4(0u, 0u, 0u, 0u);
+  int id = -1;
+  if (lane < 16 && j0 + lane < n) {
+    id = p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j0 + lane];
+    if (id < 0 || id >= p.num_blocks) {
+      record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
+      id = -1;
+    }
+  }
+  const size_t hi_off = static_cast<size_t>(p.num_kv_heads) * kChunksPerRow;
+  uint4 lo[2][4], hi[2][4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {   // rows gid, gid + 8
+    const int rid = __shfl_sync(kFullMask, id, gid + 8 * r);
+    const uint4 *src = p.bounds + (static_cast<size_t>(rid < 0 ? 0 : rid) * 2 * p.num_kv_heads + g) * kChunksPerRow + tig;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[r][i] = src[4 * i];
+      hi[r][i] = src[hi_off + 4 * i];
+    }
+  }
+  float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t qw[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+    const uint32_t l0[4] = {lo[0][i].x, lo[0][i].y, lo[0][i].z, lo[0][i].w};
+    const uint32_t l1[4] = {lo[1][i].x, lo[1][i].y, lo[1][i].z, lo[1][i].w};
+    const uint32_t h0[4] = {hi[0][i].x, hi[0][i].y, hi[0][i].z, hi[0][i].w};
+    const uint32_t h1[4] = {hi[1][i].x, hi[1][i].y, hi[1][i].z, hi[1][i].w};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // words 2k, 2k + 1 are the k slots 2 tig .. and 2 tig + 8 ..
+      const uint32_t q0 = qw[2 * k], q1 = qw[2 * k + 1];
+      const uint32_t ah[4] = {h0[2 * k], h1[2 * k], h0[2 * k + 1], h1[2 * k + 1]};
+      const uint32_t al[4] = {l0[2 * k], l1[2 * k], l0[2 * k + 1], l1[2 * k + 1]};
+      uint32_t am[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) am[e] = bound_word<T, true>(ah[e] & 0x7fff7fffu, al[e] & 0x7fff7fffu);
+      MmaType<T>::mma(s, ah, bound_word<T, true>(q0, 0u), bound_word<T, true>(q1, 0u));
+      MmaType<T>::mma(s, al, bound_word<T, false>(q0, 0u), bound_word<T, false>(q1, 0u));
+      MmaType<T>::mma(t, am, q0 & 0x7fff7fffu, q1 & 0x7fff7fffu);
+    }
+  }
+  float2 *out = p.approx + (static_cast<size_t>(b) * p.num_kv_heads + g) * p.max_blocks;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {   // s[2r], s[2r + 1]: row gid + 8 r, heads 2 tig, 2 tig + 1
+    float best = -INFINITY, most = 0.f;
+    bool odd = false;   // not finite
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * tig + e >= G) continue;
+      odd = odd || !(fabsf(s[2 * r + e]) < INFINITY) || !(t[2 * r + e] < INFINITY);
+      best = fmaxf(best, s[2 * r + e]);
+      most = fmaxf(most, t[2 * r + e]);
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      best = fmaxf(best, __shfl_xor_sync(kFullMask, best, off));
+      most = fmaxf(most, __shfl_xor_sync(kFullMask, most, off));
+      odd = __shfl_xor_sync(kFullMask, odd ? 1 : 0, off) != 0 || odd;
+    }
+    const int j = j0 + gid + 8 * r;
+    if (tig == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : most * kScoreError);
+  }
+}
+
+// fp32 caches: a half warp scores a block, lane c of it chunk c of every row.
+template <int G>
+__device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int g, int j0, int n) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  float q[G][4];
+  const uint4 *qg = static_cast<const uint4 *>(p.q) + (static_cast<size_t>(b) * p.num_heads + g * G) * kChunksPerRow + c;
+#pragma unroll
+  for (int h = 0; h < G; ++h) Elem<float>::unpack(qg[h * kChunksPerRow], q[h]);
+  float2 *out = p.approx + (static_cast<size_t>(b) * p.num_kv_heads + g) * p.max_blocks;
+#pragma unroll 2
+  for (int i = 0; i < 8; ++i) {
+    const int j = j0 + 2 * i + (lane >> 4);
+    int id = j < n ? p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j] : 0;
+    if (id < 0 || id >= p.num_blocks) {
+      if (c == 0) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
+      id = 0;
+    }
+    float lo[4], hi[4];
+    const uint4 *src = p.bounds + (static_cast<size_t>(id) * 2 * p.num_kv_heads + g) * kChunksPerRow + c;
+    Elem<float>::unpack(src[0], lo);
+    Elem<float>::unpack(src[static_cast<size_t>(p.num_kv_heads) * kChunksPerRow], hi);
+    float best = -INFINITY, most = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(q[h][e], q[h][e] >= 0.f ? hi[e] : lo[e], s);
+        t = fmaf(fabsf(q[h][e]), fmaxf(fabsf(lo[e]), fabsf(hi[e])), t);
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(kFullMask, s, off);
+        t += __shfl_xor_sync(kFullMask, t, off);
+      }
+      odd = odd || !(fabsf(s) < INFINITY) || !(t < INFINITY);
+      best = fmaxf(best, s);
+      most = fmaxf(most, t);
+    }
+    if (c == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : most * kScoreError);
+  }
+}
+
 template <typename T, int G>
 __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p) {
-  constexpr int EPC = Elem<T>::kPerChunk;
   pdl_wait();
   pdl_trigger();
   int item = blockIdx.x;
@@ -145,92 +272,98 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
     return;
   }
   const int n = (L + kBlockSize - 1) / kBlockSize;
-  if (n <= p.num_selected) return;   // every block is chosen
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  const int half = (threadIdx.x >> 5) * 2 + (lane >> 4);
-  float q[G][EPC];
-  const uint4 *qg = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q)) +
-                    (static_cast<size_t>(b) * p.num_heads + g * G) * kChunksPerRow + c;
-#pragma unroll
-  for (int h = 0; h < G; ++h) Elem<T>::unpack(qg[h * kChunksPerRow], q[h]);
-  const int32_t *bt = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq;
-  unsigned long long *keys = p.keys + (static_cast<size_t>(b) * p.num_kv_heads + g) * p.max_blocks;
-  for (int i = 0; i < kScoreBlocks; i += 2 * kScoreWarps) {
-    const int j = chunk * kScoreBlocks + i + half;
-    const int id = j < n ? bt[j] : 0;
-    const bool good = j < n && id >= 0 && id < p.num_blocks;
-    if (j < n && !good && c == 0) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
-    float lo[EPC], hi[EPC];
-    {
-      const uint4 *src = p.bounds + (static_cast<size_t>(good ? id : 0) * 2 * p.num_kv_heads + g) * kChunksPerRow + c;
-      Elem<T>::unpack(src[0], lo);
-      Elem<T>::unpack(src[static_cast<size_t>(p.num_kv_heads) * kChunksPerRow], hi);
-    }
-    double best = 0.0;
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-      double s = 0.0;
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) {
-        const float k = q[h][e] >= 0.f ? hi[e] : lo[e];
-        s = fma(static_cast<double>(q[h][e]), static_cast<double>(k), s);
-      }
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(kFullMask, s, off);
-      best = h == 0 || s > best || s != s ? s : best;   // a NaN stays: no later score is larger than it
-    }
-    if (c == 0 && j < n) keys[j] = good ? score_key(best) : 0ull;
-  }
+  const int j0 = chunk * kScoreBlocks + (threadIdx.x >> 5) * 16;
+  if (n <= p.num_selected || j0 >= n) return;   // every block is chosen, or none is left for this warp
+  if constexpr (sizeof(T) == 4) score_tile_f32<G>(p, b, g, j0, n);
+  else score_tile<T, G>(p, b, g, j0, n);
 }
 
 // ---------------------------------------------------------------- choice
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectBins = 2048;
+constexpr int kSelectCached = 4096;     // fp32 scores kept in shared memory (more are read again from L2)
+constexpr int kSelectDoubt = 1024;      // blocks in doubt that the fast path takes
+constexpr int kSelectMaxBlocks = 65536; // blocks that the fast path takes (a bit each)
 
-// Exclusive sum of `flag` over the CTA's threads, and the total.
-__device__ __forceinline__ int block_rank(bool flag, int *warp_s, int &total) {
+// The fp64 score of block j, by a warp; every lane gets it.
+template <typename T, int G>
+__device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, int b, int g, int j) {
+  constexpr int D = kChunksPerRow * Elem<T>::kPerChunk;
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int id = p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j];
+  if (id < 0 || id >= p.num_blocks) return 0ull;   // recorded by the score kernel
+  const T *lo = reinterpret_cast<const T *>(p.bounds) + (static_cast<size_t>(id) * 2 * p.num_kv_heads + g) * D + lane * E;
+  const T *hi = lo + static_cast<size_t>(p.num_kv_heads) * D;
+  const T *q = static_cast<const T *>(p.q) + (static_cast<size_t>(b) * p.num_heads + g * G) * D + lane * E;
+  unsigned long long best = 0ull;
+#pragma unroll 1
+  for (int h = 0; h < G; ++h) {
+    double s = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float x = Elem<T>::load(q + h * D + e);
+      s = fma(static_cast<double>(x), static_cast<double>(Elem<T>::load((x >= 0.f ? hi : lo) + e)), s);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFullMask, s, off);
+    const unsigned long long key = score_key(s);
+    best = h == 0 || key > best ? key : best;
+  }
+  return best;
+}
+
+// Exclusive sum of `x` over the CTA's threads, and the total.
+__device__ __forceinline__ int block_sum(int x, int *warp_s, int &total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned bits = __ballot_sync(kFullMask, flag);
+  int upto = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(kFullMask, upto, off);
+    if (lane >= off) upto += y;
+  }
   __syncthreads();   // warp_s of the previous call has been read
-  if (lane == 0) warp_s[warp] = __popc(bits);
+  if (lane == 31) warp_s[warp] = upto;
   __syncthreads();
   int before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
+  for (int w = 0; w < kSelectWarps; ++w) {
     before += w < warp ? warp_s[w] : 0;
     total += warp_s[w];
   }
-  return before + __popc(bits & ((1u << lane) - 1u));
+  return before + upto - x;
 }
 
-// A CTA per (sequence, KV head): the first `sink` and last `recent` blocks and,
-// of the others, those of the largest keys -- a radix select that narrows the
-// smallest chosen key 8 bits at a time -- written in ascending order, ties to the
-// lowest index; -1 behind them.
-__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const SelectParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_s[kSelectThreads / 32];
-  __shared__ int found_digit, found_above;
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.x / p.num_kv_heads;
-  const int K = p.num_selected;
-  const int L = p.context_lens[b];
-  int32_t *out = p.selected + static_cast<size_t>(blockIdx.x) * K;
-  const unsigned long long *keys = p.keys + static_cast<size_t>(blockIdx.x) * p.max_blocks;
-  const bool bad = L < 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize;
-  const int n = bad ? 0 : (L + kBlockSize - 1) / kBlockSize;   // a bad length: an empty list
-  if (n <= K) {
-    if (bad && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
-    for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < n ? i : -1;
-    return;
+// Largest of `x` over the CTA's threads.
+__device__ __forceinline__ float block_max(float x, float *warp_s) {
+  const float m = warp_max(x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_s[threadIdx.x >> 5] = m;
+  __syncthreads();
+  float r = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) r = fmaxf(r, warp_s[w]);
+  return r;
+}
+
+// The `need` largest fp64 scores of blocks j0 .. j1-1, ties to the lowest index, for lists
+// that the fast path does not take: fp64 scores of all of them, then a radix select
+// that narrows the smallest chosen key 8 bits at a time, then the list itself.
+template <typename T, int G>
+__device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int g, int n, int j0, int j1, int need,
+                                              unsigned long long *keys, int32_t *out, int *hist, int *warp_s,
+                                              int *found) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j = j0 + warp; j < j1; j += kSelectWarps) {
+    const unsigned long long key = exact_key<T, G>(p, b, g, j);
+    if (lane == 0) keys[j] = key;
   }
-  const int j0 = p.sink, j1 = n - p.recent;   // n > K >= sink + recent
-  int need = K - p.sink - p.recent;           // of the blocks j0 .. j1 - 1
-  // chosen: key >> shift above `prefix`, and the first `need` of those equal to it
+  __syncthreads();
   unsigned long long prefix = 0;
   int shift = 64;
-  while (need > 0 && shift > 0) {
+  while (shift > 0) {
     for (int i = threadIdx.x; i < 256; i += kSelectThreads) hist[i] = 0;
     __syncthreads();
     for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
@@ -238,48 +371,199 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
       if (shift == 64 || (key >> shift) == prefix) atomicAdd(&hist[(key >> (shift - 8)) & 255], 1);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {   // the digit that the need-th largest key has
-      const int lane = threadIdx.x;
-      int mine = 0;   // lane l: digits 255 - 8 l down to 248 - 8 l
-#pragma unroll
-      for (int d = 0; d < 8; ++d) mine += hist[255 - 8 * lane - d];
-      int upto = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(kFullMask, upto, off);
-        if (lane >= off) upto += x;
-      }
-      int above = upto - mine;
-      if (above < need && upto >= need) {
-        int d = 255 - 8 * lane;
-        while (above + hist[d] < need) above += hist[d--];
-        found_digit = d;
-        found_above = above;
-      }
+    if (threadIdx.x == 0) {   // the digit that the need-th largest key has
+      int d = 255, above = 0;
+      while (above + hist[d] < need) above += hist[d--];
+      found[0] = d;
+      found[1] = above;
     }
     __syncthreads();
-    need -= found_above;
-    prefix = shift == 64 ? found_digit : (prefix << 8) | found_digit;
+    need -= found[1];
+    prefix = shift == 64 ? found[0] : (prefix << 8) | found[0];
     shift -= 8;
-    const bool whole = hist[found_digit] == need;   // every key with this prefix is chosen
     __syncthreads();
-    if (whole) break;
   }
   int written = 0, equal_before = 0;
   for (int base = 0; base < n; base += kSelectThreads) {
     const int j = base + threadIdx.x;
     bool take = j < n && (j < j0 || j >= j1), equal = false;
-    if (j >= j0 && j < j1 && K > p.sink + p.recent) {
-      const unsigned long long high = keys[j] >> shift;
-      take = high > prefix;
-      equal = high == prefix;
+    if (j >= j0 && j < j1) {
+      take = keys[j] > prefix;
+      equal = keys[j] == prefix;
     }
     int total;
-    const int rank = block_rank(equal, warp_s, total);
+    const int rank = block_sum(equal ? 1 : 0, warp_s, total);
     if (equal && equal_before + rank < need) take = true;
     equal_before += total;
-    const int at = block_rank(take, warp_s, total);
+    const int at = block_sum(take ? 1 : 0, warp_s, total);
     if (take) out[written + at] = j;
+    written += total;
+  }
+}
+
+// A CTA per (sequence, KV head): the first `sink` and last `recent` blocks and,
+// of the others, those of the largest scores, in ascending order; -1 behind them.
+// With E the largest error bound and the need-th largest fp32 score within [t0, t1]
+// (the scores of its bin of an even histogram), the need-th largest score is within
+// [t0 - E, t1 + E]: an fp32 score above t1 + 2 E is chosen, one below t0 - 2 E is not,
+// and only the rest is in doubt and ranked by fp64 scores.
+template <typename T, int G>
+__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const SelectParams p) {
+  __shared__ union {
+    int hist[kSelectBins];
+    unsigned bits[kSelectMaxBlocks / 32];   // chosen blocks
+  } u;
+  __shared__ float score_s[kSelectCached];
+  __shared__ unsigned long long doubt_key[kSelectDoubt];
+  __shared__ int doubt_j[kSelectDoubt];
+  __shared__ int warp_s[kSelectWarps];
+  __shared__ float warp_f[kSelectWarps];
+  __shared__ int found[2];
+  __shared__ int num_doubt, num_in;
+  static_assert(kSelectMaxBlocks / 32 <= kSelectBins, "the bits take the histogram's place");
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x % p.num_kv_heads;
+  const int b = blockIdx.x / p.num_kv_heads;
+  const int K = p.num_selected;
+  const int L = p.context_lens[b];
+  int32_t *out = p.selected + static_cast<size_t>(blockIdx.x) * K;
+  const bool bad = L < 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize;
+  const int n = bad ? 0 : (L + kBlockSize - 1) / kBlockSize;   // a bad length: an empty list
+  if (n <= K) {
+    if (bad && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
+    for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < n ? i : -1;
+    return;
+  }
+  const float2 *approx = p.approx + static_cast<size_t>(blockIdx.x) * p.max_blocks;
+  const int j0 = p.sink, j1 = n - p.recent;   // n > K >= sink + recent
+  const int need = K - p.sink - p.recent;     // of the blocks j0 .. j1 - 1
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // ---- range and error of the fp32 scores; NaN marks the blocks that are in doubt anyway
+  float top = -INFINITY, low = INFINITY, err = 0.f, odd = 0.f;
+  for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+    const float2 x = approx[j];
+    const bool fine = x.y < INFINITY;
+    if (j < kSelectCached) score_s[j] = fine ? x.x : __int_as_float(0x7fffffff);
+    if (fine) {
+      top = fmaxf(top, x.x);
+      low = fminf(low, x.x);
+      err = fmaxf(err, x.y);
+    } else {
+      odd = 1.f;
+    }
+  }
+  for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) u.hist[i] = 0;
+  if (threadIdx.x == 0) {
+    num_doubt = num_in = 0;
+    found[0] = -1;
+  }
+  top = block_max(top, warp_f);
+  low = -block_max(-low, warp_f);
+  err = 2.f * block_max(err, warp_f);
+  const bool any_odd = block_max(odd, warp_f) > 0.f;
+  const float width = top - low;
+  const float scale = width > 0.f && width < INFINITY ? (kSelectBins - 1) / width : 0.f;
+  auto score = [&](int j) {
+    if (j < kSelectCached) return score_s[j];
+    const float2 x = approx[j];
+    return x.y < INFINITY ? x.x : __int_as_float(0x7fffffff);
+  };
+  auto bin = [&](float x) { return min(kSelectBins - 1, static_cast<int>((x - low) * scale)); };   // grows with x
+  float t0 = -INFINITY, t1 = INFINITY;   // no block with a finite score: all are in doubt
+  if (need > 0) {
+    for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+      const float x = score(j);
+      if (x == x) atomicAdd(&u.hist[bin(x)], 1);
+    }
+    __syncthreads();
+    // the bin of the need-th largest (thread t: bins from the top down, 4 t .. 4 t + 3)
+    constexpr int kPer = kSelectBins / kSelectThreads;
+    int mine = 0;
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) mine += u.hist[kSelectBins - 1 - kPer * threadIdx.x - d];
+    int total;
+    int above = block_sum(mine, warp_s, total);
+    if (above < need && above + mine >= need) {
+      int d = kSelectBins - 1 - kPer * threadIdx.x;
+      while (above + u.hist[d] < need) above += u.hist[d--];
+      found[0] = d;
+    }
+    __syncthreads();
+    const int at = found[0];
+    float a = INFINITY, z = -INFINITY;
+    if (at >= 0) {
+      for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+        const float x = score(j);
+        if (x == x && bin(x) == at) {
+          a = fminf(a, x);
+          z = fmaxf(z, x);
+        }
+      }
+      t0 = -block_max(-a, warp_f) - err;
+      t1 = block_max(z, warp_f) + err;
+    }
+  }
+  __syncthreads();
+  // ---- chosen, not chosen, in doubt.  (Blocks without a finite fp32 score may be above any other
+  // and take its place: with some, nothing is certain to be chosen; what is below t0 is still out.)
+  for (int i = threadIdx.x; i < kSelectMaxBlocks / 32 && i * 32 < n; i += kSelectThreads) u.bits[i] = 0u;
+  __syncthreads();
+  const bool fast = n <= kSelectMaxBlocks;
+  for (int base = j0; base < j1 && need > 0 && fast; base += kSelectThreads) {
+    const int j = base + threadIdx.x;
+    const float x = j < j1 ? score(j) : -INFINITY;
+    const bool in = j < j1 && !any_odd && x > t1;
+    const bool doubt = j < j1 && !in && !(x < t0);
+    if (in) {
+      atomicAdd(&num_in, 1);
+      atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+    }
+    if (doubt) {
+      const int at = atomicAdd(&num_doubt, 1);
+      if (at < kSelectDoubt) doubt_j[at] = j;
+    }
+  }
+  __syncthreads();
+  const int m = num_doubt;
+  const int left = need - num_in;   // how many of the blocks in doubt are chosen
+  if (need > 0 && (!fast || m > kSelectDoubt || left < 0)) {
+    __syncthreads();
+    select_all_exact<T, G>(p, b, g, n, j0, j1, need, p.keys + static_cast<size_t>(blockIdx.x) * p.max_blocks, out,
+                           u.hist, warp_s, found);
+    return;
+  }
+  if (!fast) {   // need == 0: the first and last blocks alone
+    for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < j0 ? i : n - K + i;
+    return;
+  }
+  if (m > left) {
+    for (int i = warp; i < m; i += kSelectWarps) {
+      const unsigned long long key = exact_key<T, G>(p, b, g, doubt_j[i]);
+      if (lane == 0) doubt_key[i] = key;
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < m; i += kSelectThreads) {
+    const int j = doubt_j[i];
+    int before = 0;   // blocks in doubt that are chosen before this one
+    if (m > left) {
+      const unsigned long long key = doubt_key[i];
+      for (int k = 0; k < m; ++k) before += doubt_key[k] > key || (doubt_key[k] == key && doubt_j[k] < j);
+    }
+    if (before < left) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+  }
+  for (int j = threadIdx.x; j < j0; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+  for (int j = j1 + threadIdx.x; j < n; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+  __syncthreads();
+  // ---- the list
+  int written = 0;
+  const int words = (n + 31) / 32;
+  for (int base = 0; base < words; base += kSelectThreads) {
+    unsigned w = base + threadIdx.x < words ? u.bits[base + threadIdx.x] : 0u;
+    int total;
+    int at = written + block_sum(__popc(w), warp_s, total);
+    for (; w != 0u; w &= w - 1u) out[at++] = (base + threadIdx.x) * 32 + __ffs(w) - 1;
     written += total;
   }
 }

@@ -144,6 +144,42 @@ def test_choice_takes_nan_blocks_first(pa):
     assert torch.equal(got, want) and {11, 20, 40} <= set(got[0, 0].tolist())
 
 
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+@pytest.mark.parametrize("n,kinds,K", [(3000, 2, 700), (5000, 1, 1500), (70000, 3, 40), (70000, 70000, 40)])
+def test_choice_of_many_blocks_and_ties(pa, ty, n, kinds, K):
+    """More ties than the fast path takes, more blocks than its cache (4096) and its bits (65536) hold."""
+    d = ref.HEAD_DIM[ty]
+    lens = torch.tensor([n * 16], dtype=torch.int32)
+    g = torch.Generator().manual_seed(n + kinds)
+    base = torch.randn((min(kinds, 1000), 2, 1, d), generator=g).to(ref.TYPES[ty])
+    base = torch.stack([base.amin(1), base.amax(1)], 1)
+    tables = (torch.arange(n) % base.shape[0])[None].int()       # blocks of equal content are one block
+    q = ref.make_q(1, 2, ty, seed=n)
+    x = q[0].double()[:, None]
+    rows = base[:, :, 0].double()
+    score = (x * torch.where(x >= 0, rows[:, 1], rows[:, 0])).sum(-1).amax(0)[torch.arange(n) % base.shape[0]]
+    score[0] = score[-2:] = float("inf")
+    want = torch.argsort(score, descending=True, stable=True)[:K].sort().values.int()
+    got = pa.select_blocks(*cuda(q, base, tables, lens), K, sink_blocks=1, recent_blocks=2)
+    assert torch.equal(got.cpu()[0, 0], want)
+
+
+def test_choice_with_scores_that_overflow_fp32(pa):
+    """Products beyond fp32: their blocks are ranked in 64 bits like the others."""
+    n = 300
+    lens = torch.tensor([n * 16], dtype=torch.int32)
+    tables = torch.arange(n, dtype=torch.int32)[None]
+    g = torch.Generator().manual_seed(2)
+    bounds = torch.randn((n, 2, 1, 128), generator=g).bfloat16()
+    bounds = torch.stack([bounds.amin(1), bounds.amax(1)], 1)
+    bounds[::7] *= 2.0 ** 120
+    q = (torch.randn((1, 4, 128), generator=g) * 2.0 ** 20).bfloat16()
+    for K in (5, 43, 44, 60):
+        want = ref.choose(q, bounds, tables, lens, K, 0, 1)
+        got = pa.select_blocks(*cuda(q, bounds, tables, lens), K, sink_blocks=0, recent_blocks=1)
+        assert torch.equal(got.cpu(), want), K
+
+
 @pytest.mark.expects_device_error
 def test_choice_reports_bad_input(pa):
     k, _, tables, lens = ref.make_cache([200, 300], 1, "bf16", seed=4)
