@@ -346,61 +346,65 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block
 # These wrappers run on the tensors' device (which need not be the current one)
 # and allocate what the caller left out on the stream that the call runs on.
 
-def _one_device(**tensors: torch.Tensor) -> torch.device:
-    device = None
-    for name, t in tensors.items():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    return device
+# They are called once a layer and step, so the checks are a single pass and the
+# messages are put together only when one fails.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _flat(**tensors: torch.Tensor) -> None:
-    for name, t in tensors.items():
-        if not t.is_contiguous():
+def _device_of(names: str, tensors, flat: int) -> int:
+    """The device index that all tensors (named in `names`) are on; the first `flat` must be contiguous too."""
+    index = tensors[0].get_device()
+    for i, t in enumerate(tensors):
+        if t.get_device() != index or index < 0 or (i < flat and not t.is_contiguous()):
+            name = names.split()[i]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, {names.split()[0]} on {tensors[0].device}")
             raise ValueError(f"{name} must be contiguous")
+    return index
 
 
-def _launch(fn, where: str, device: torch.device, stream: Optional[torch.cuda.Stream], *args) -> None:
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, s.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, s.cuda_stream)
-    _check(status, where)
-
-
-def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _launch(fn, where: str, index: int, stream: Optional[torch.cuda.Stream], *args) -> None:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        raw = _raw_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        raw = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != 0:
+        raise PaError(status, where)
+
+
+def _empty(shape, dtype: torch.dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
-def _bytes_of(fn, device: torch.device, *args: int) -> int:
+def _bytes_of(fn, index: int, *args: int) -> int:
     """A workspace size, which may depend on the device's SM count."""
-    if device.index == torch.cuda.current_device():
+    if index == torch.cuda.current_device():
         return int(fn(*args))
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return int(fn(*args))
 
 
-def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device,
-               stream: Optional[torch.cuda.Stream]):
+def _workspace(need: int, workspace: Optional[torch.Tensor], index: int, stream: Optional[torch.cuda.Stream]):
     """(tensor, pointer, bytes); the tensor has to live until the launch is queued."""
     if workspace is None:
         if not need:
             return None, None, 0
-        workspace = _empty(need, torch.uint8, device, stream)
-    elif workspace.device != device or not workspace.is_contiguous():
+        workspace = _empty(need, torch.uint8, index, stream)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the other tensors' device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0,
@@ -411,19 +415,19 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0,
         raise ValueError("device must be a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    table = _empty((max(max_position, 0), max(rotary_dim, 0)), torch.float32, device, stream)
-    _launch(_lib.pa_rope_table, "pa_rope_table", device, stream, table.data_ptr(), max_position, rotary_dim, float(base))
+    table = _empty((max(max_position, 0), max(rotary_dim, 0)), torch.float32, device.index, stream)
+    _launch(_lib.pa_rope_table, "pa_rope_table", device.index, stream, table.data_ptr(), max_position, rotary_dim, float(base))
     return table
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the token rows of [T, heads, D]; heads and D must be contiguous."""
-    T, h, d = t.shape
+def _row_stride(t: torch.Tensor, name: str, T: int, h: int, d: int) -> int:
+    """Elements between the token rows of [T, h, d]; heads and d must be contiguous."""
     if T == 0:
         return h * d
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if T > 1 else h * d
+    return s0 if T > 1 else h * d
 
 
 def _rope(fn, where, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping, q_out, interleaved, stream,
@@ -434,24 +438,26 @@ def _rope(fn, where, q, key, value, positions, cos_sin, k_cache, v_cache, slot_m
     T, hq, _ = q.shape
     if key.dtype != q.dtype or value.dtype != q.dtype:
         raise ValueError("q, key and value must have one dtype")
-    if tuple(key.shape) != (T, hkv, d) or tuple(value.shape) != (T, hkv, d):
+    kv = (T, hkv, d)
+    if key.shape != kv or value.shape != kv:
         raise ValueError("key/value must be [T, num_kv_heads, head_dim]")
     if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or positions.numel() != T or \
             slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping must be int64 [T]")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim] float32")
-    device = _one_device(q=q, key=key, value=value, positions=positions, cos_sin=cos_sin, k_cache=k_cache,
-                         v_cache=v_cache, slot_mapping=slot_mapping)
-    _flat(positions=positions, cos_sin=cos_sin, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
+    index = _device_of("k_cache v_cache positions cos_sin slot_mapping q key value",
+                       (k_cache, v_cache, positions, cos_sin, slot_mapping, q, key, value), 5)
     if q_out is None:
-        q_out = _empty((T, hq, d), q.dtype, device, stream)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != device:
+        q_out = _empty((T, hq, d), q.dtype, index, stream)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != index:
         raise ValueError("q_out must match q")
-    _launch(fn, where, device, stream, q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(),
+    max_position, rotary = cos_sin.shape
+    _launch(fn, where, index, stream, q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), slot_mapping.data_ptr(), T,
-            _row_stride(q_out, "q_out"), _row_stride(q, "q"), _row_stride(key, "key"), _row_stride(value, "value"),
-            cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, nb, bs, hq, hkv, d, dtype_code, *scales)
+            _row_stride(q_out, "q_out", T, hq, d), _row_stride(q, "q", T, hq, d), _row_stride(key, "key", T, hkv, d),
+            _row_stride(value, "value", T, hkv, d), max_position, rotary, 1 if interleaved else 0, nb, bs, hq, hkv, d,
+            dtype_code, *scales)
     return q_out
 
 
@@ -491,10 +497,10 @@ def _decode_inputs(q, block_tables, context_lens, d: int, dtype: torch.dtype):
     return S, hq
 
 
-def _out_like(q, out, device, stream):
+def _out_like(q, out, index, stream):
     if out is None:
-        return _empty(q.shape, q.dtype, device, stream)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != device or not out.is_contiguous():
+        return _empty(q.shape, q.dtype, index, stream)
+    if out.shape != q.shape or out.dtype != q.dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must match q and be contiguous")
     return out
 
@@ -520,10 +526,8 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     n = prefix_lens.numel()
     if group_start.dtype != torch.int32 or prefix_lens.dtype != torch.int32 or group_start.numel() != n + 1:
         raise ValueError("group_start and prefix_lens must be int32 [G + 1] and [G]")
-    device = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-                         group_start=group_start, prefix_lens=prefix_lens)
-    _flat(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-          group_start=group_start, prefix_lens=prefix_lens)
+    index = _device_of("q k_cache v_cache block_tables context_lens group_start prefix_lens",
+                        (q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens), 7)
     if max_prefix_len is None or max_suffix_len is None or max_group_size is None:
         starts, prefixes = group_start.cpu().long(), prefix_lens.cpu().long()
         sizes = (starts[1:] - starts[:-1]).clamp(min=0)
@@ -536,13 +540,13 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
             if int(sizes.sum()) == S:
                 own = own - prefixes.repeat_interleave(sizes)
             max_suffix_len = max(0, int(own.max())) if S else 0
-    out = _out_like(q, out, device, stream)
+    out = _out_like(q, out, index, stream)
     need = 0
     if workspace is None:
-        need = _bytes_of(_lib.pa_decode_shared_prefix_workspace_bytes, device, S, n, hq, hkv, d, max_prefix_len,
+        need = _bytes_of(_lib.pa_decode_shared_prefix_workspace_bytes, index, S, n, hq, hkv, d, max_prefix_len,
                          max_suffix_len, max_group_size)
-    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
-    _launch(_lib.pa_decode_shared_prefix, "pa_decode_shared_prefix", device, stream, out.data_ptr(), q.data_ptr(),
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, index, stream)
+    _launch(_lib.pa_decode_shared_prefix, "pa_decode_shared_prefix", index, stream, out.data_ptr(), q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
             context_lens.data_ptr(), group_start.data_ptr(), prefix_lens.data_ptr(), S, n, hq, max_prefix_len,
             max_suffix_len, max_group_size, float(scale), ws_ptr, ws_bytes, nb, bs, hkv, d, dt)
@@ -550,7 +554,7 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
 
 def _bounds_args(block_bounds, nb, hkv, d, dtype):
-    if tuple(block_bounds.shape) != (nb, 2, hkv, d) or block_bounds.dtype != dtype:
+    if block_bounds.shape != (nb, 2, hkv, d) or block_bounds.dtype != dtype:
         raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim] with the cache dtype")
 
 
@@ -566,13 +570,11 @@ def update_block_bounds(k_cache: torch.Tensor, block_bounds: torch.Tensor, block
         raise ValueError("block_tables, context_lens and new_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or new_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq], context_lens and new_lens [S]")
-    device = _one_device(k_cache=k_cache, block_bounds=block_bounds, block_tables=block_tables,
-                         context_lens=context_lens, new_lens=new_lens)
-    _flat(k_cache=k_cache, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens,
-          new_lens=new_lens)
+    index = _device_of("k_cache block_bounds block_tables context_lens new_lens",
+                        (k_cache, block_bounds, block_tables, context_lens, new_lens), 5)
     if max_new_len is None:
         max_new_len = int(new_lens.max()) if S else 0
-    _launch(_lib.pa_update_block_bounds, "pa_update_block_bounds", device, stream, k_cache.data_ptr(),
+    _launch(_lib.pa_update_block_bounds, "pa_update_block_bounds", index, stream, k_cache.data_ptr(),
             block_bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
             new_lens.data_ptr(), S, max_new_len, nb, bs, hkv, d, dt)
 
@@ -591,18 +593,17 @@ def select_blocks(q: torch.Tensor, block_bounds: torch.Tensor, block_tables: tor
         raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim]")
     nb, _, hkv, d = block_bounds.shape
     S, hq = _decode_inputs(q, block_tables, context_lens, d, block_bounds.dtype)
-    device = _one_device(q=q, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens)
-    _flat(q=q, block_bounds=block_bounds, block_tables=block_tables, context_lens=context_lens)
+    index = _device_of("q block_bounds block_tables context_lens", (q, block_bounds, block_tables, context_lens), 4)
     if isinstance(selected, int):
-        selected = _empty((S, hkv, max(selected, 0)), torch.int32, device, stream)
-    elif selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, hkv) or \
-            selected.device != device or not selected.is_contiguous():
+        selected = _empty((S, hkv, max(selected, 0)), torch.int32, index, stream)
+    elif selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, hkv) or \
+            selected.get_device() != index or not selected.is_contiguous():
         raise ValueError("selected must be a contiguous int32 [S, num_kv_heads, K]")
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
     need = _lib.pa_select_blocks_workspace_bytes(S, hkv, max_context_len) if workspace is None else 0
-    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
-    _launch(_lib.pa_select_blocks, "pa_select_blocks", device, stream, selected.data_ptr(), q.data_ptr(),
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, index, stream)
+    _launch(_lib.pa_select_blocks, "pa_select_blocks", index, stream, selected.data_ptr(), q.data_ptr(),
             block_bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, hq,
             max_context_len, selected.shape[2], sink_blocks, recent_blocks, ws_ptr, ws_bytes, nb, 16, hkv, d,
             DTYPE_CODE[q.dtype])
@@ -621,19 +622,17 @@ def decode_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Paged decode over the blocks of ``selected`` (int32 [S, Hkv, K] distinct logical indices, < 0 = none) only."""
     nb, bs, hkv, d, dt = _cache_args(k_cache, v_cache)
     S, hq = _decode_inputs(q, block_tables, context_lens, d, k_cache.dtype)
-    if selected.dtype != torch.int32 or selected.dim() != 3 or tuple(selected.shape[:2]) != (S, hkv):
+    if selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, hkv):
         raise ValueError("selected must be int32 [S, num_kv_heads, K]")
     K = selected.shape[2]
-    device = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-                         selected=selected)
-    _flat(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-          selected=selected)
-    out = _out_like(q, out, device, stream)
+    index = _device_of("q k_cache v_cache block_tables context_lens selected",
+                        (q, k_cache, v_cache, block_tables, context_lens, selected), 6)
+    out = _out_like(q, out, index, stream)
     need = 0
     if workspace is None:
-        need = _bytes_of(_lib.pa_decode_selected_workspace_bytes, device, S, hq, hkv, d, K)
-    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, device, stream)
-    _launch(_lib.pa_decode_selected, "pa_decode_selected", device, stream, out.data_ptr(), q.data_ptr(),
+        need = _bytes_of(_lib.pa_decode_selected_workspace_bytes, index, S, hq, hkv, d, K)
+    workspace, ws_ptr, ws_bytes = _workspace(need, workspace, index, stream)
+    _launch(_lib.pa_decode_selected, "pa_decode_selected", index, stream, out.data_ptr(), q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
             context_lens.data_ptr(), selected.data_ptr(), S, hq, K, float(scale), ws_ptr, ws_bytes, nb, bs, hkv, d, dt)
     return out

@@ -1117,16 +1117,28 @@ pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block
 
 namespace {
 
-// Blocks a partition of a selected-block decode: enough CTAs for two waves of
-// three an SM, from 4 blocks (one a warp) to 64.
+// Tokens a partition of a selected-block decode: a multiple of 4 blocks (one a warp)
+// that gives the shortest run, in units of a block a warp: a wave of three CTAs an SM
+// takes its share of a partition's blocks plus about two blocks' time of set-up
+// and merge, and every partition adds a partial to combine.
 int selected_partition(int num_seqs, int num_kv_heads, int num_selected) {
-  const long long want = 6LL * sm_count();
   const long long pairs = (long long)num_seqs * num_kv_heads;
-  long long parts = (want + pairs - 1) / pairs;
-  long long blocks = (num_selected + parts - 1) / parts;
-  if (blocks < 4) blocks = 4;
-  if (blocks > 64) blocks = 64;
-  return (int)(blocks + 3) / 4 * 4 * kBlockSize;
+  const long long slots = 3LL * sm_count();
+  double best = 1e300;
+  int blocks = 4;
+  for (int parts = 1; parts <= 64 && (parts == 1 || 4 * (parts - 1) < num_selected); ++parts) {
+    const int per = ((num_selected + parts - 1) / parts + 3) / 4 * 4;
+    const int n = (num_selected + per - 1) / per;
+    // a last wave that is not full runs faster: it counts for at least half
+    const double full = (double)(pairs * n / slots), rest = (double)(pairs * n % slots) / slots;
+    const double waves = full + (rest > 0 ? (rest > 0.5 ? rest : 0.5) : 0.0);
+    const double cost = (waves < 1 ? 1 : waves) * (per / 4 + 2) + 0.25 * n;
+    if (cost < best) {
+      best = cost;
+      blocks = per;
+    }
+  }
+  return blocks * kBlockSize;
 }
 
 template <typename T, int G, typename Math>

@@ -286,7 +286,8 @@ constexpr int kSelectCached = 4096;     // fp32 scores kept in shared memory (mo
 constexpr int kSelectDoubt = 1024;      // blocks in doubt that the fast path takes
 constexpr int kSelectMaxBlocks = 65536; // blocks that the fast path takes (a bit each)
 
-// The fp64 score of block j, by a warp; every lane gets it.
+// The fp64 score of block j, by a warp; every lane gets it.  Lane l holds elements
+// E l .. of every row; all loads are in flight at once.
 template <typename T, int G>
 __device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, int b, int g, int j) {
   constexpr int D = kChunksPerRow * Elem<T>::kPerChunk;
@@ -294,23 +295,34 @@ __device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, i
   const int lane = threadIdx.x & 31;
   const int id = p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j];
   if (id < 0 || id >= p.num_blocks) return 0ull;   // recorded by the score kernel
-  const T *lo = reinterpret_cast<const T *>(p.bounds) + (static_cast<size_t>(id) * 2 * p.num_kv_heads + g) * D + lane * E;
-  const T *hi = lo + static_cast<size_t>(p.num_kv_heads) * D;
-  const T *q = static_cast<const T *>(p.q) + (static_cast<size_t>(b) * p.num_heads + g * G) * D + lane * E;
-  unsigned long long best = 0ull;
-#pragma unroll 1
+  struct alignas(8) Row {
+    T x[E];
+  };
+  const Row *bounds = reinterpret_cast<const Row *>(p.bounds);
+  const Row lo = bounds[(static_cast<size_t>(id) * 2 * p.num_kv_heads + g) * 32 + lane];
+  const Row hi = bounds[(static_cast<size_t>(id) * 2 * p.num_kv_heads + p.num_kv_heads + g) * 32 + lane];
+  const Row *qg = static_cast<const Row *>(p.q) + (static_cast<size_t>(b) * p.num_heads + g * G) * 32 + lane;
+  Row q[G];
+#pragma unroll
+  for (int h = 0; h < G; ++h) q[h] = qg[h * 32];
+  double s[G];
+#pragma unroll
   for (int h = 0; h < G; ++h) {
-    double s = 0.0;
+    s[h] = 0.0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float x = Elem<T>::load(q + h * D + e);
-      s = fma(static_cast<double>(x), static_cast<double>(Elem<T>::load((x >= 0.f ? hi : lo) + e)), s);
+      const float x = Elem<T>::load(&q[h].x[e]);
+      const float k = x >= 0.f ? Elem<T>::load(&hi.x[e]) : Elem<T>::load(&lo.x[e]);
+      s[h] = fma(static_cast<double>(x), static_cast<double>(k), s[h]);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFullMask, s, off);
-    const unsigned long long key = score_key(s);
-    best = h == 0 || key > best ? key : best;
   }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int h = 0; h < G; ++h) s[h] += __shfl_xor_sync(kFullMask, s[h], off);
+  unsigned long long best = score_key(s[0]);
+#pragma unroll
+  for (int h = 1; h < G; ++h) best = max(best, score_key(s[h]));
   return best;
 }
 
@@ -336,16 +348,14 @@ __device__ __forceinline__ int block_sum(int x, int *warp_s, int &total) {
   return before + upto - x;
 }
 
-// Largest of `x` over the CTA's threads.
-__device__ __forceinline__ float block_max(float x, float *warp_s) {
-  const float m = warp_max(x);
+// Element-wise largest of `x` over the CTA's threads.
+__device__ __forceinline__ float4 block_max(float4 x, float4 *warp_f) {
+  x = make_float4(warp_max(x.x), warp_max(x.y), warp_max(x.z), warp_max(x.w));
+  __syncthreads();   // warp_f of the previous call has been read
+  if ((threadIdx.x & 31) == 0) warp_f[threadIdx.x >> 5] = x;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) warp_s[threadIdx.x >> 5] = m;
-  __syncthreads();
-  float r = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) r = fmaxf(r, warp_s[w]);
-  return r;
+  const float4 y = warp_f[threadIdx.x & (kSelectWarps - 1)];
+  return make_float4(warp_max(y.x), warp_max(y.y), warp_max(y.z), warp_max(y.w));
 }
 
 // The `need` largest fp64 scores of blocks j0 .. j1-1, ties to the lowest index, for lists
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   __shared__ unsigned long long doubt_key[kSelectDoubt];
   __shared__ int doubt_j[kSelectDoubt];
   __shared__ int warp_s[kSelectWarps];
-  __shared__ float warp_f[kSelectWarps];
+  __shared__ float4 warp_f[kSelectWarps];
   __shared__ int found[2];
   __shared__ int num_doubt, num_in;
   static_assert(kSelectMaxBlocks / 32 <= kSelectBins, "the bits take the histogram's place");
@@ -458,10 +468,11 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     num_doubt = num_in = 0;
     found[0] = -1;
   }
-  top = block_max(top, warp_f);
-  low = -block_max(-low, warp_f);
-  err = 2.f * block_max(err, warp_f);
-  const bool any_odd = block_max(odd, warp_f) > 0.f;
+  const float4 range = block_max(make_float4(top, -low, err, odd), warp_f);
+  top = range.x;
+  low = -range.y;
+  err = 2.f * range.z;
+  const bool any_odd = range.w > 0.f;
   const float width = top - low;
   const float scale = width > 0.f && width < INFINITY ? (kSelectBins - 1) / width : 0.f;
   auto score = [&](int j) {
@@ -500,8 +511,9 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
           z = fmaxf(z, x);
         }
       }
-      t0 = -block_max(-a, warp_f) - err;
-      t1 = block_max(z, warp_f) + err;
+      const float4 edge = block_max(make_float4(-a, z, 0.f, 0.f), warp_f);
+      t0 = -edge.x - err;
+      t1 = edge.y + err;
     }
   }
   __syncthreads();
