@@ -1141,17 +1141,22 @@ int selected_partition(int num_seqs, int num_kv_heads, int num_selected) {
   return blocks * kBlockSize;
 }
 
-template <typename T, int G, typename Math>
+template <typename T, int G, typename Math, int W = pa::kDecodeWarps>
 pa_status_t launch_selected(const CUtensorMap &mk, const CUtensorMap &mv, const pa::SelectedParams &p,
                             cudaStream_t stream) {
-  using SM = pa::DecodeSmem<T, G, Math>;
-  auto kernel = pa::pa_decode_partition_kernel<T, G, Math, pa::kDecodeWarps, pa::kWalkSelected>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) != cudaSuccess)
-    return PA_ERR_CUDA;
   const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.max_partitions;
   if (grid > INT32_MAX) return PA_ERR_SHAPE;
-  const pa_status_t st =
-      launch(kernel, dim3((unsigned)grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, p);
+  // More CTAs than a wave of three an SM: two-warp CTAs, six an SM, where the block
+  // math has them (61 sequences x 8 heads of 33 blocks: 62.1 us a pass of choice and
+  // decode against 67.9; within one wave four warps are faster, 19.1 against 20.4 at 64 CTAs).
+  if constexpr (W == pa::kDecodeWarps && !Math::kNeedsQInSmem) {
+    if (grid > 3LL * sm_count()) return launch_selected<T, G, Math, 2>(mk, mv, p, stream);
+  }
+  using SM = pa::DecodeSmem<T, G, Math, W>;
+  auto kernel = pa::pa_decode_partition_kernel<T, G, Math, W, pa::kWalkSelected>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) != cudaSuccess)
+    return PA_ERR_CUDA;
+  const pa_status_t st = launch(kernel, dim3((unsigned)grid), dim3(W * 32), SM::kAlloc, stream, mk, mv, p);
   if (st != PA_OK || p.max_partitions <= 1) return st;
   const long long rows = (long long)p.num_seqs * p.num_heads;
   long long ctas = (rows + pa::kReduceWarps - 1) / pa::kReduceWarps;

@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(kRopeTokens * kRopeHeads * kRopeItems) rope_an
       const T *base = static_cast<const T *>(is_q ? p.q : is_k ? p.key : p.value) +
                       tok * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride);
       const uint4 *src = reinterpret_cast<const uint4 *>(base) + hl * kChunksPerRow;
-      x0[u] = src[c0];
-      x1[u] = src[c1];
+      x0[u] = NH > 1 ? __ldcs(src + c0) : src[c0];
+      x1[u] = NH > 1 ? __ldcs(src + c1) : src[c1];
     }
   }
   if (pos < 0) return;   // padding token: nothing is written
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kRopeTokens * kRopeHeads * kRopeItems) rope_an
     uint4 *dst = is_q ? reinterpret_cast<uint4 *>(static_cast<T *>(p.q_out) + tok * p.q_out_stride) + hl * kChunksPerRow
                       : reinterpret_cast<uint4 *>(is_k ? p.k_cache : p.v_cache) +
                             (slot * p.num_kv_heads + hl) * kChunksPerRow;
-    // Rows of a large batch are written with the streaming hint: 32.5 us against 34.7
-    // at 8192 tokens (97% of the copy bandwidth).  A small batch's stay in L2 for the attention.
+    // Rows of a large batch are read and written with the streaming hint: 32.5 us against
+    // 34.7 at 8192 tokens (97% of the copy bandwidth).  A small batch's stay in L2 for the attention.
     if (NH > 1) {
       __stcs(dst + c0, x0[u]);
       __stcs(dst + c1, x1[u]);

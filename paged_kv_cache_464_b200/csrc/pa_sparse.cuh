@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 // block_score_kernel gives every block an fp32 score with a bound on its error, and
 // block_select_kernel computes fp64 scores only for the blocks that the bound leaves in
 // doubt.  fp64 scores of all blocks cost 80 us for 8 x 8 x 2048 blocks and 8 heads
-// (two conversions to fp64 for each product, 16 a cycle and SM), against NEWSCORE.
+// (two conversions to fp64 for each product, 16 a cycle and SM), against 17.
 struct SelectParams {
   const void *q;                  // [S][Hq][D]
   const uint4 *bounds;            // [NB][2][Hkv][16 chunks]
