@@ -805,9 +805,13 @@ struct PrefixPlan {
   WorkspaceLayout ws;
 };
 
-// Partitions: as many as give the shortest run, in units of half a tile's time: a
-// wave of one CTA an SM takes the tiles of its longest partition plus about five
-// tiles' time of set-up and epilogue, and each partition adds a partial to combine.
+// Partitions: as many as give the shortest run by this model, in us measured on B200.  A
+// CTA (one an SM) takes 8.5 of set-up and epilogue and 2.9 a step; a step is a
+// tile, or two where a CTA has at most 128 rows.  A last wave that is not full counts for
+// at least half.  Each partition's partials cost 0.35 to combine and their
+// bytes, written and read.  (47 sequences in three groups, 32 KV heads: 45.2 a call with
+// the two partitions chosen, 57.1 with one, 54.5 with three; 128 sequences over 1024 tokens:
+// 41.0 with four, 41.7 with eight; 5 over 4000: 18.2 with eight, 19.2 with sixteen.)
 PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_prefix_len,
                        int max_suffix_len, int max_group_size) {
   PrefixPlan r{};
@@ -816,14 +820,17 @@ PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_h
   r.row_ctas = (rows + 2 * pa::kPrefixRows - 1) / (2 * pa::kPrefixRows);
   const int tiles = (max_prefix_len + pa::kPrefixKv - 1) / pa::kPrefixKv;
   if (tiles > 0) {
-    const long long ctas = (long long)num_groups * r.row_ctas * num_kv_heads;
-    const int sms = sm_count();
-    long long best = INT64_MAX;
+    const double ctas = (double)num_groups * r.row_ctas * num_kv_heads;
+    const double sms = sm_count();
+    const double partial_us = 0.35 + (double)num_seqs * num_heads * 2 * head_dim * sizeof(float) / 6.5e6;
+    double best = 1e300;
     int per = tiles;
     for (int parts = 1; parts <= tiles && parts <= 64; ++parts) {
       const int t = (tiles + parts - 1) / parts;
-      const long long waves = (ctas * parts + sms - 1) / sms;
-      const long long cost = waves * (2 * t + 10) + parts;
+      const int steps = rows <= pa::kPrefixRows ? (t + 1) / 2 : t;
+      const double waves = ctas * parts / sms, full = std::floor(waves), rest = waves - full;
+      const double runs = waves <= 1 ? 1 : full + (rest > 0 ? (rest > 0.5 ? rest : 0.5) : 0);
+      const double cost = runs * (8.5 + 2.9 * steps) + parts * partial_us;
       if (cost < best) {
         best = cost;
         per = t;
