@@ -351,18 +351,15 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _device_of(names: str, tensors, flat: int) -> int:
-    """The device index that all tensors (named in `names`) are on; the first `flat` must be contiguous too."""
-    index = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if t.get_device() != index or index < 0 or (i < flat and not t.is_contiguous()):
-            name = names.split()[i]
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if t.get_device() != index:
-                raise ValueError(f"{name} is on {t.device}, {names.split()[0]} on {tensors[0].device}")
+def _refuse(names: str, tensors, flat: int) -> None:
+    """Say which of the tensors is not where the first one is, or (the first `flat` of them) not contiguous."""
+    for i, (name, t) in enumerate(zip(names.split(), tensors)):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != tensors[0].get_device():
+            raise ValueError(f"{name} is on {t.device}, {names.split()[0]} on {tensors[0].device}")
+        if i < flat and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    return index
 
 
 def _launch(fn, where: str, index: int, stream: Optional[torch.cuda.Stream], *args) -> None:
@@ -432,25 +429,30 @@ def _row_stride(t: torch.Tensor, name: str, T: int, h: int, d: int) -> int:
 
 def _rope(fn, where, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping, q_out, interleaved, stream,
           dtype_code, *scales):
-    nb, bs, hkv, d, _ = _cache_args(k_cache, v_cache)
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q must be [T, num_heads, head_dim]")
-    T, hq, _ = q.shape
-    if key.dtype != q.dtype or value.dtype != q.dtype:
-        raise ValueError("q, key and value must have one dtype")
-    kv = (T, hkv, d)
-    if key.shape != kv or value.shape != kv:
-        raise ValueError("key/value must be [T, num_kv_heads, head_dim]")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, num_kv_heads, head_dim]")
+    nb, bs, hkv, d = k_cache.shape
+    if q.dim() != 3 or key.shape != value.shape or key.dim() != 3:
+        raise ValueError("q must be [T, num_heads, head_dim], key and value [T, num_kv_heads, head_dim]")
+    T, hq, dq = q.shape
+    dtype = q.dtype
+    if dq != d or key.shape != (T, hkv, d) or key.dtype != dtype or value.dtype != dtype:
+        raise ValueError("q [T, num_heads, head_dim], key and value [T, num_kv_heads, head_dim] must have one dtype")
     if positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64 or positions.numel() != T or \
             slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping must be int64 [T]")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim] float32")
-    index = _device_of("k_cache v_cache positions cos_sin slot_mapping q key value",
-                       (k_cache, v_cache, positions, cos_sin, slot_mapping, q, key, value), 5)
+    index = k_cache.get_device()
+    if not (0 <= index == v_cache.get_device() == positions.get_device() == cos_sin.get_device()
+            == slot_mapping.get_device() == q.get_device() == key.get_device() == value.get_device()
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and positions.is_contiguous()
+            and cos_sin.is_contiguous() and slot_mapping.is_contiguous()):
+        _refuse("k_cache v_cache positions cos_sin slot_mapping q key value",
+                (k_cache, v_cache, positions, cos_sin, slot_mapping, q, key, value), 5)
     if q_out is None:
-        q_out = _empty((T, hq, d), q.dtype, index, stream)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != index:
+        q_out = _empty((T, hq, d), dtype, index, stream)
+    elif q_out.shape != q.shape or q_out.dtype != dtype or q_out.get_device() != index:
         raise ValueError("q_out must match q")
     max_position, rotary = cos_sin.shape
     _launch(fn, where, index, stream, q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(),
@@ -526,8 +528,14 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     n = prefix_lens.numel()
     if group_start.dtype != torch.int32 or prefix_lens.dtype != torch.int32 or group_start.numel() != n + 1:
         raise ValueError("group_start and prefix_lens must be int32 [G + 1] and [G]")
-    index = _device_of("q k_cache v_cache block_tables context_lens group_start prefix_lens",
-                        (q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens), 7)
+    index = q.get_device()
+    if not (0 <= index == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == context_lens.get_device() == group_start.get_device() == prefix_lens.get_device()
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and group_start.is_contiguous()
+            and prefix_lens.is_contiguous()):
+        _refuse("q k_cache v_cache block_tables context_lens group_start prefix_lens",
+                (q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens), 7)
     if max_prefix_len is None or max_suffix_len is None or max_group_size is None:
         starts, prefixes = group_start.cpu().long(), prefix_lens.cpu().long()
         sizes = (starts[1:] - starts[:-1]).clamp(min=0)
@@ -553,25 +561,28 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return out
 
 
-def _bounds_args(block_bounds, nb, hkv, d, dtype):
-    if block_bounds.shape != (nb, 2, hkv, d) or block_bounds.dtype != dtype:
-        raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim] with the cache dtype")
-
-
 def update_block_bounds(k_cache: torch.Tensor, block_bounds: torch.Tensor, block_tables: torch.Tensor,
                         context_lens: torch.Tensor, new_lens: torch.Tensor, *, max_new_len: Optional[int] = None,
                         stream: Optional[torch.cuda.Stream] = None) -> None:
     """Smallest and largest key per channel, ``block_bounds`` [NB, 2, Hkv, D], of every block that holds one of a
     sequence's last ``new_lens`` (int32 [S]) tokens."""
-    nb, bs, hkv, d, dt = _cache_args(k_cache, k_cache)
-    _bounds_args(block_bounds, nb, hkv, d, k_cache.dtype)
+    if k_cache.dim() != 4 or k_cache.dtype not in DTYPE_CODE:
+        raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim], fp32, fp16 or bf16")
+    nb, bs, hkv, d = k_cache.shape
+    dt = DTYPE_CODE[k_cache.dtype]
+    if block_bounds.shape != (nb, 2, hkv, d) or block_bounds.dtype != k_cache.dtype:
+        raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim] with the cache dtype")
     S = context_lens.numel()
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or new_lens.dtype != torch.int32:
         raise ValueError("block_tables, context_lens and new_lens must be int32")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or new_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq], context_lens and new_lens [S]")
-    index = _device_of("k_cache block_bounds block_tables context_lens new_lens",
-                        (k_cache, block_bounds, block_tables, context_lens, new_lens), 5)
+    index = k_cache.get_device()
+    if not (0 <= index == block_bounds.get_device() == block_tables.get_device() == context_lens.get_device()
+            == new_lens.get_device() and k_cache.is_contiguous() and block_bounds.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and new_lens.is_contiguous()):
+        _refuse("k_cache block_bounds block_tables context_lens new_lens",
+                (k_cache, block_bounds, block_tables, context_lens, new_lens), 5)
     if max_new_len is None:
         max_new_len = int(new_lens.max()) if S else 0
     _launch(_lib.pa_update_block_bounds, "pa_update_block_bounds", index, stream, k_cache.data_ptr(),
@@ -593,7 +604,11 @@ def select_blocks(q: torch.Tensor, block_bounds: torch.Tensor, block_tables: tor
         raise ValueError("block_bounds must be [num_blocks, 2, num_kv_heads, head_dim]")
     nb, _, hkv, d = block_bounds.shape
     S, hq = _decode_inputs(q, block_tables, context_lens, d, block_bounds.dtype)
-    index = _device_of("q block_bounds block_tables context_lens", (q, block_bounds, block_tables, context_lens), 4)
+    index = q.get_device()
+    if not (0 <= index == block_bounds.get_device() == block_tables.get_device() == context_lens.get_device()
+            and q.is_contiguous() and block_bounds.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous()):
+        _refuse("q block_bounds block_tables context_lens", (q, block_bounds, block_tables, context_lens), 4)
     if isinstance(selected, int):
         selected = _empty((S, hkv, max(selected, 0)), torch.int32, index, stream)
     elif selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, hkv) or \
@@ -625,8 +640,13 @@ def decode_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (S, hkv):
         raise ValueError("selected must be int32 [S, num_kv_heads, K]")
     K = selected.shape[2]
-    index = _device_of("q k_cache v_cache block_tables context_lens selected",
-                        (q, k_cache, v_cache, block_tables, context_lens, selected), 6)
+    index = q.get_device()
+    if not (0 <= index == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+            == context_lens.get_device() == selected.get_device() and q.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and selected.is_contiguous()):
+        _refuse("q k_cache v_cache block_tables context_lens selected",
+                (q, k_cache, v_cache, block_tables, context_lens, selected), 6)
     out = _out_like(q, out, index, stream)
     need = 0
     if workspace is None:

@@ -256,6 +256,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
   };
   if (warp >= kPrefixLoadWarp) load_ids(0);
+  // the 16 boxes of an item: eight blocks (ids one a lane from `first`), two halves of their rows
+  auto load_tile = [&](int st, const CUtensorMap *tm, int first) {
+    int ids[8];
+#pragma unroll
+    for (int bi = 0; bi < 8; ++bi) ids[bi] = __shfl_sync(kFullMask, my_id, first + bi);
+    if (lane == 0) {
+      uint8_t *dst = stage_ptr(st);
+      mbar_arrive_expect_tx(&full[st], SM::kTile);
+#pragma unroll
+      for (int bi = 0; bi < 8; ++bi)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          tma_load_5d(dst + half * SM::kHalf + bi * (kBlockSize * 128), tm, 0, half, g, 0, ids[bi], &full[st]);
+    }
+  };
+  // K tile 0 is on its way before Q is in place (this warp set the barriers up)
+  if (warp == kPrefixLoadWarp && !stall_here) load_tile(0, &tm_k, 0);   // (test hook: left unissued)
   // ---- Q -> shared memory, K-major 128-byte swizzled: [d half][row][128 B]; warpgroup w its tile
   if (warp < kPrefixMmaWarp && (warp < 4 || !split)) {
     const int w = warp >> 2;
@@ -292,29 +309,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int n = tiles_of(w);
       const int base = ring_base(w);
       int grp = 0;
+      int st = 0, phase = 0;   // it % ring_len, it / ring_len & 1
       for (int it = 0; it < 2 * n; ++it) {   // item it: K (even) or V (odd) of this ring's tile it / 2
-        const int st = it % ring_len;
         if (it >= ring_len &&
-            !__all_sync(kFullMask, role_wait(&free_[base + st], (it / ring_len - 1) & 1, abort_s, wait_limit)))
+            !__all_sync(kFullMask, role_wait(&free_[base + st], phase ^ 1, abort_s, wait_limit)))
           break;
         const int j = split ? 2 * (it >> 1) + w : it >> 1;
         if (((8 * j) >> 5) != grp) {
           grp = (8 * j) >> 5;
           load_ids(grp);
         }
-        int ids[8];
-#pragma unroll
-        for (int bi = 0; bi < 8; ++bi) ids[bi] = __shfl_sync(kFullMask, my_id, (8 * j + bi) & 31);
-        if (lane == 0 && !(stall_here && it == 0 && w == 0)) {   // (test hook: K tile 0 left unissued)
-          uint8_t *dst = stage_ptr(base + st);
-          uint64_t *bar = &full[base + st];
-          const CUtensorMap *tm = (it & 1) ? &tm_v : &tm_k;
-          mbar_arrive_expect_tx(bar, SM::kTile);
-#pragma unroll
-          for (int bi = 0; bi < 8; ++bi)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              tma_load_5d(dst + half * SM::kHalf + bi * (kBlockSize * 128), tm, 0, half, g, 0, ids[bi], bar);
+        if (it > 0 || w > 0) load_tile(base + st, (it & 1) ? &tm_v : &tm_k, (8 * j) & 31);   // w = 0: K tile 0 above
+        if (++st == ring_len) {
+          st = 0;
+          phase ^= 1;
         }
         issued = it + 1;
       }
@@ -344,24 +352,34 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const uint64_t k_desc = smem_desc_sw128(stage_ptr(base), 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(stage_ptr(base), SM::kHalf, 1024);
       const uint32_t s_tmem = tmem + w * 256, o_tmem = s_tmem + 128;
+      // Stages and phases are counted along: a division by ring_len is a chain through the
+      // exponent unit, behind the softmax's exponentials (several hundred cycles).
+      int st = 0, phase = 0;
+      auto next = [&]() {
+        if (++st == ring_len) {
+          st = 0;
+          phase ^= 1;
+        }
+      };
       for (int i = 0; i < n && ok; ++i) {
-        const int sk = (2 * i) % ring_len, sv = (2 * i + 1) % ring_len;
-        wait(&full[base + sk], (2 * i / ring_len) & 1);
+        wait(&full[base + st], phase);
         if (i > 0) wait(&tb[3], (i - 1) & 1);   // PV(i-1) has read P from S's columns
         if (!ok) break;
-        const uint64_t b0 = k_desc + ((sk * SM::kTile) >> 4);
+        const uint64_t b0 = k_desc + ((st * SM::kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_f16(s_tmem, a0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4),
                    b0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
         umma_commit(&tb[0]);
-        wait(&full[base + sv], ((2 * i + 1) / ring_len) & 1);
+        next();
+        wait(&full[base + st], phase);
         if (i > 0 || w > 0) {   // PV_0(i) follows PV_1(i-1), PV_1(i) follows PV_0(i)
           const int before = w > 0 ? i : i - 1;
           if (before < n_other) wait(&turn[w], before & 1);
         }
         if (!ok) break;
-        const uint64_t v0 = v_desc + ((sv * SM::kTile) >> 4);
+        const uint64_t v0 = v_desc + ((st * SM::kTile) >> 4);
+        next();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           wait(&tb[1 + hf], i & 1);   // the half's P written
@@ -406,15 +424,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
+    const int base = ring_base(w);
+    int st = 0;   // stage of the next item to free
     for (int i = 0; i < n && ok; ++i) {
       wait(&tb[0], i & 1);
       if (!ok) break;
       // QK(i) is complete, and so is PV(i-1), which it waited for: their stages are free
-      if ((tid & 127) == 0) {
-        const int base = ring_base(w);
-        mbar_arrive(&free_[base + 2 * i % ring_len]);
-        if (i > 0) mbar_arrive(&free_[base + (2 * i - 1) % ring_len]);
+      if (i > 0) {
+        if ((tid & 127) == 0) mbar_arrive(&free_[base + st]);   // item 2 i - 1
+        st = st + 1 == ring_len ? 0 : st + 1;
       }
+      if ((tid & 127) == 0) mbar_arrive(&free_[base + st]);     // item 2 i
+      st = st + 1 == ring_len ? 0 : st + 1;
       float s[128];
       tmem_ld64(t_s, *reinterpret_cast<float (*)[64]>(s));
       tmem_ld64(t_s + 64, *reinterpret_cast<float (*)[64]>(s + 64));
