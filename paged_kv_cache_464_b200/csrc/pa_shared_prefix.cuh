@@ -73,19 +73,32 @@ static_assert(2 * kPrefixRows * 512 <= PrefixSmem::kBar, "staged rows");
 static_assert(2 + kPrefixStagesPair <= PrefixSmem::kTiles && 1 + 2 * kPrefixStagesSplit <= PrefixSmem::kTiles, "tiles");
 
 // Bounded wait of the hand-overs between roles.  The timer is first read after 32
-// polls: reading %globaltimer costs hundreds of cycles, which a wait that is
-// about to end must not pay.
+// polls (reading %globaltimer costs hundreds of cycles, which a wait that is about to
+// end must not pay), and out of line: every wait's code counts (see the kernel).
+// The start of the wait (t0, 0 at first), or 0 once it has to end.
+__device__ __noinline__ unsigned long long wait_goes_on(unsigned long long t0, const volatile int *abort_flag,
+                                                        int stall_cta) {
+  const unsigned long long now = global_ns();
+  if (t0 == 0) t0 = now;
+  return *abort_flag || now - t0 > wait_limit_for(stall_cta, blockIdx.x) ? 0 : t0;
+}
+
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort_flag,
-                                          unsigned long long limit_ns) {
+                                          int stall_cta) {
   unsigned long long t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
     if ((it & 31u) == 0) {
-      const unsigned long long now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (*abort_flag || now - t0 > limit_ns) return false;
+      t0 = wait_goes_on(t0, abort_flag, stall_cta);
+      if (t0 == 0) return false;
     }
   }
+  return true;
+}
+
+// A wait ran out: recorded, and the CTA's other roles are told.
+__device__ __noinline__ void give_up(volatile int *abort_flag) {
+  record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, blockIdx.x);
+  *abort_flag = 1;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -128,34 +141,34 @@ __device__ __forceinline__ float row_max(const float *s) {
   return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
-// P = 2^((s - m) c2) of 64 scores -> tensor memory at taddr: 32 columns of pairs (the
-// upper 16 bits as they are for bf16, rounded for fp16) and, for bf16, 32 columns
-// of what those leave, rounded.  Returns two partial sums of P.
+// P = 2^((s - m) c2) of the 32 scores in columns taddr .. taddr + 31, written over them: 16
+// columns of pairs (the upper 16 bits as they are for bf16, rounded for fp16)
+// and, for bf16, 16 columns of what those leave, rounded.  Scores from `live` on
+// count for nothing.  Adds the sums of even and odd columns to `sum`.
 template <typename PK, bool kLo>
-__device__ __forceinline__ float2 exp_half(const float *s, float c2, float m, uint32_t taddr) {
-  const float2 nmc = make_float2(-m * c2, -m * c2);
-  const float2 cc2 = make_float2(c2, c2);
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+__device__ __forceinline__ void exp_chunk(uint32_t taddr, int live, float2 cc2, float2 nmc, float2 &sum) {
+  float s[32];
+  tmem_ld32(taddr, s);
+  if (live < 32) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t hi[16], lo[kLo ? 16 : 1];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float2 x = __ffma2_rn(make_float2(s[32 * q + 2 * k], s[32 * q + 2 * k + 1]), cc2, nmc);
-      const float2 e = make_float2(ex2(x.x), ex2(x.y));
-      sum[k & 1] = __fadd2_rn(sum[k & 1], e);
-      if constexpr (kLo) {
-        const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
-        hi[k] = __byte_perm(ux, uy, 0x7632);
-        lo[k] = PK::pack(e.x - __uint_as_float(ux & 0xffff0000u), e.y - __uint_as_float(uy & 0xffff0000u));
-      } else {
-        hi[k] = PK::pack(e.x, e.y);
-      }
-    }
-    tmem_st16u(taddr + 16 * q, hi);
-    if constexpr (kLo) tmem_st16u(taddr + 32 + 16 * q, lo);
+    for (int k = 0; k < 32; ++k) s[k] = k < live ? s[k] : -INFINITY;
   }
-  return __fadd2_rn(sum[0], sum[1]);
+  uint32_t hi[16], lo[kLo ? 16 : 1];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), cc2, nmc);
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    sum = __fadd2_rn(sum, e);
+    if constexpr (kLo) {
+      const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
+      hi[k] = __byte_perm(ux, uy, 0x7632);
+      lo[k] = PK::pack(e.x - __uint_as_float(ux & 0xffff0000u), e.y - __uint_as_float(uy & 0xffff0000u));
+    } else {
+      hi[k] = PK::pack(e.x, e.y);
+    }
+  }
+  tmem_st16u(taddr, hi);
+  if constexpr (kLo) tmem_st16u(taddr + 16, lo);
 }
 
 template <typename T, int G>
@@ -173,16 +186,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   uint64_t *free_ = full + 6;
   uint64_t *tile_bars = free_ + 6;   // w: s_full, p_half, p_full, o_done at 4 w
   uint64_t *drain = tile_bars + 8;
-  uint64_t *turn = drain + 1;        // [w]: the other's PV that w's next one follows is issued
+  uint64_t *turn = drain + 1;        // [w]: the PV of the other that w's next one follows is issued
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::kTmemSlot);
   volatile int *abort_s = reinterpret_cast<int *>(smem + SM::kFlag);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const long long cta = blockIdx.x;
-  const unsigned long long wait_limit = wait_limit_for(p.stall_cta, cta);
-  const bool stall_here = p.stall_cta != 0 && cta == p.stall_cta - 1;
+  const bool stall_here = p.stall_cta != 0 && static_cast<int>(blockIdx.x) == p.stall_cta - 1;
   if (warp == kPrefixLoadWarp && lane == 0) {
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
@@ -237,6 +248,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     mbar_init(drain, 2);
     mbar_init(&turn[0], 1);
     mbar_init(&turn[1], 1);
+
     fence_mbar_init();
     *abort_s = 0;
   }
@@ -258,17 +270,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   if (warp >= kPrefixLoadWarp) load_ids(0);
   // the 16 boxes of an item: eight blocks (ids one a lane from `first`), two halves of their rows
   auto load_tile = [&](int st, const CUtensorMap *tm, int first) {
-    int ids[8];
-#pragma unroll
-    for (int bi = 0; bi < 8; ++bi) ids[bi] = __shfl_sync(kFullMask, my_id, first + bi);
-    if (lane == 0) {
-      uint8_t *dst = stage_ptr(st);
-      mbar_arrive_expect_tx(&full[st], SM::kTile);
-#pragma unroll
-      for (int bi = 0; bi < 8; ++bi)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          tma_load_5d(dst + half * SM::kHalf + bi * (kBlockSize * 128), tm, 0, half, g, 0, ids[bi], &full[st]);
+    uint8_t *dst = stage_ptr(st);
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], SM::kTile);
+#pragma unroll 1
+    for (int bi = 0; bi < 8; ++bi) {
+      const int id = __shfl_sync(kFullMask, my_id, first + bi);
+      if (lane == 0) {
+        tma_load_5d(dst + bi * (kBlockSize * 128), tm, 0, 0, g, 0, id, &full[st]);
+        tma_load_5d(dst + SM::kHalf + bi * (kBlockSize * 128), tm, 0, 1, g, 0, id, &full[st]);
+      }
     }
   };
   // K tile 0 is on its way before Q is in place (this warp set the barriers up)
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       int st = 0, phase = 0;   // it % ring_len, it / ring_len & 1
       for (int it = 0; it < 2 * n; ++it) {   // item it: K (even) or V (odd) of this ring's tile it / 2
         if (it >= ring_len &&
-            !__all_sync(kFullMask, role_wait(&free_[base + st], phase ^ 1, abort_s, wait_limit)))
+            !__all_sync(kFullMask, role_wait(&free_[base + st], phase ^ 1, abort_s, p.stall_cta)))
           break;
         const int j = split ? 2 * (it >> 1) + w : it >> 1;
         if (((8 * j) >> 5) != grp) {
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (lane == 0) {
       // ================================================================ tensor-core issue for w
       const int w = warp - kPrefixMmaWarp;
-      const int n = tiles_of(w), n_other = tiles_of(1 - w);
+      const int n = tiles_of(w);
       const int base = ring_base(w);
       uint64_t *tb = tile_bars + 4 * w;
       constexpr uint32_t kIdescQK = instr_desc_f16(PK::kFormat, false, kPrefixRows, kPrefixKv);
@@ -339,11 +349,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       bool ok = true;
       auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
-        ok = role_wait(bar, parity, abort_s, wait_limit);
-        if (!ok) {
-          record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
-          *abort_s = 1;
-        }
+        ok = role_wait(bar, parity, abort_s, p.stall_cta);
+        if (!ok) give_up(abort_s);
         tc_fence_after();
       };
       // an operand at byte offset `off` from a tile's base has the base's descriptor
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (i > 0) wait(&tb[3], (i - 1) & 1);   // PV(i-1) has read P from S's columns
         if (!ok) break;
         const uint64_t b0 = k_desc + ((st * SM::kTile) >> 4);
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < D / 16; ++kk)
           umma_f16(s_tmem, a0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4),
                    b0 + (((kk >> 2) * SM::kHalf + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
@@ -375,20 +382,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         wait(&full[base + st], phase);
         if (i > 0 || w > 0) {   // PV_0(i) follows PV_1(i-1), PV_1(i) follows PV_0(i)
           const int before = w > 0 ? i : i - 1;
-          if (before < n_other) wait(&turn[w], before & 1);
+          if (before < tiles_of(1 - w)) wait(&turn[w], before & 1);
         }
         if (!ok) break;
         const uint64_t v0 = v_desc + ((st * SM::kTile) >> 4);
         next();
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           wait(&tb[1 + hf], i & 1);   // the half's P written
           if (!ok) break;
 #pragma unroll
           for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {   // 16 tokens = 8 columns of P a step
-            const uint32_t p_tmem = s_tmem + 64 * hf + (kk & 3) * 8;
+            const uint32_t p_tmem = s_tmem + 32 * (kk >> 1) + 8 * (kk & 1);   // 16 columns of P, 16 of its low parts
             umma_f16_ts(o_tmem, p_tmem, v0 + ((kk * 16 * 128) >> 4), kIdescPV, i > 0 || kk > 0);
-            if constexpr (kLo) umma_f16_ts(o_tmem, p_tmem + 32, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
+            if constexpr (kLo) umma_f16_ts(o_tmem, p_tmem + 16, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
           }
         }
         if (!ok) break;
@@ -411,11 +418,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (!ok) return;
-      ok = __all_sync(kFullMask, role_wait(bar, parity, abort_s, wait_limit));
-      if (!ok && lane == 0) {
-        record_error(5 /*PA_DEV_WAIT_TIMEOUT*/, cta);
-        *abort_s = 1;
-      }
+      ok = __all_sync(kFullMask, role_wait(bar, parity, abort_s, p.stall_cta));
+      if (!ok && lane == 0) give_up(abort_s);
       tc_fence_after();
     };
     auto hand_over = [&](uint64_t *bar) {   // this warp's P is in tensor memory
@@ -436,38 +440,44 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       }
       if ((tid & 127) == 0) mbar_arrive(&free_[base + st]);     // item 2 i
       st = st + 1 == ring_len ? 0 : st + 1;
-      float s[128];
-      tmem_ld64(t_s, *reinterpret_cast<float (*)[64]>(s));
-      tmem_ld64(t_s + 64, *reinterpret_cast<float (*)[64]>(s + 64));
       const int live = tokens - (split ? 2 * i + w : i) * kPrefixKv;   // a multiple of 16
-      if (live < kPrefixKv) {
+      float tmax;
+      {
+        float s[128];
+        tmem_ld64(t_s, *reinterpret_cast<float (*)[64]>(s));
+        tmem_ld64(t_s + 64, *reinterpret_cast<float (*)[64]>(s + 64));
+        if (live < kPrefixKv) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c < live ? s[c] : -INFINITY;
+          for (int c = 0; c < 128; ++c) s[c] = c < live ? s[c] : -INFINITY;
+        }
+        tmax = row_max<128>(s);
       }
-      if (i == 0) m_run = row_max<128>(s);
       // m_run, the reference of the exponentials, follows only a score that passes it by more than 2^8
-      if (i > 0) {
-        const float tmax = row_max<128>(s);
-        const bool need = (tmax - m_run) * c2 > kRescaleLog2;
-        if (__any_sync(kFullMask, need)) {
-          // O, complete up to tile i-1 (QK(i) was issued after PV(i-1)), follows
-          const float f = need ? ex2((m_run - tmax) * c2) : 1.f;
-          if (need) m_run = tmax;
-          l_run *= f;
+      const bool need = i > 0 && (tmax - m_run) * c2 > kRescaleLog2;
+      if (__any_sync(kFullMask, need)) {
+        // O, complete up to tile i-1 (QK(i) was issued after PV(i-1)), follows
+        const float f = need ? ex2((m_run - tmax) * c2) : 1.f;
+        l_run *= f;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(t_o + c, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            tmem_st32(t_o + c, o);
-          }
+          for (int k = 0; k < 32; ++k) o[k] *= f;
+          tmem_st32(t_o + c, o);
         }
       }
-      float2 sum = exp_half<PK, kLo>(s, c2, m_run, t_s);
-      hand_over(&tb[1]);
-      sum = __fadd2_rn(sum, exp_half<PK, kLo>(s + 64, c2, m_run, t_s + 64));
-      hand_over(&tb[2]);
+      if (i == 0 || need) m_run = tmax;
+      // The scores are read a second time, 32 a turn of a short loop: with all 128 in line the
+      // kernel was 68 KB of instructions, which its roles (and the neighbouring SM's) evict
+      // from the cache between them: 83.7 us a call against 75.2 (64 sequences x 32768 tokens).
+      const float2 nmc = make_float2(-m_run * c2, -m_run * c2), cc2 = make_float2(c2, c2);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int c = 0; c < 4; ++c) {
+        exp_chunk<PK, kLo>(t_s + 32 * c, live - 32 * c, cc2, nmc, sum);
+        if (c & 1) hand_over(&tb[1 + (c >> 1)]);
+      }
       l_run += sum.x + sum.y;
     }
     // ---- this warp's 32 rows of partials: m in base-2 units, o and l relative to it.  In
@@ -507,13 +517,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   __syncthreads();
   if ((warp == kPrefixMmaWarp || warp == kPrefixMmaWarp + 1) && lane == 0) {
     umma_commit(drain);
-    mbar_wait(drain, 0, wait_limit);
+    mbar_wait(drain, 0, wait_limit_for(p.stall_cta, blockIdx.x));
   }
   if (*abort_s && warp >= kPrefixLoadWarp && lane == 0) {
     // the last item issued into each stage (an earlier one's copy landed before its stage was reissued)
     const int w = warp - kPrefixLoadWarp;
     for (int it = max(0, issued - ring_len); it < issued; ++it)
-      if (!(stall_here && it == 0 && w == 0)) mbar_wait(&full[ring_base(w) + it % ring_len], (it / ring_len) & 1, wait_limit);
+      if (!(stall_here && it == 0 && w == 0)) mbar_wait(&full[ring_base(w) + it % ring_len], (it / ring_len) & 1,
+                  wait_limit_for(p.stall_cta, blockIdx.x));
   }
   __syncthreads();
   if (warp == kPrefixMmaWarp) {
