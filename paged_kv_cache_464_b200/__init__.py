@@ -10,6 +10,8 @@ __all__ = ["capi", "inputs"]
 
 def __getattr__(name):
     if name in ("reshape_and_cache", "decode", "copy_blocks", "decode_workspace_bytes",
+                "rope_table", "rope_and_cache", "rope_and_cache_fp8", "decode_shared_prefix",
+                "update_block_bounds", "select_blocks", "decode_selected",
                 "get_device_error", "PaError"):
         from . import capi
         return getattr(capi, name)

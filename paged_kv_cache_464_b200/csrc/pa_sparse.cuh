@@ -289,7 +289,7 @@ constexpr int kSelectMaxBlocks = 65536; // blocks that the fast path takes (a bi
 // The fp64 score of block j, by a warp; every lane gets it.  Lane l holds elements
 // E l .. of every row; all loads are in flight at once.
 template <typename T, int G>
-__device__ __forceinline__ unsigned long long exact_key(const SelectParams &p, int b, int g, int j) {
+__device__ __noinline__ unsigned long long exact_key(const SelectParams &p, int b, int g, int j) {
   constexpr int D = kChunksPerRow * Elem<T>::kPerChunk;
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -366,6 +366,7 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
                                               unsigned long long *keys, int32_t *out, int *hist, int *warp_s,
                                               int *found) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int j = j0 + warp; j < j1; j += kSelectWarps) {
     const unsigned long long key = exact_key<T, G>(p, b, g, j);
     if (lane == 0) keys[j] = key;
@@ -374,8 +375,10 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
   unsigned long long prefix = 0;
   int shift = 64;
   while (shift > 0) {
+#pragma unroll 1
     for (int i = threadIdx.x; i < 256; i += kSelectThreads) hist[i] = 0;
     __syncthreads();
+#pragma unroll 1
     for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
       const unsigned long long key = keys[j];
       if (shift == 64 || (key >> shift) == prefix) atomicAdd(&hist[(key >> (shift - 8)) & 255], 1);
@@ -394,6 +397,7 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
     __syncthreads();
   }
   int written = 0, equal_before = 0;
+#pragma unroll 1
   for (int base = 0; base < n; base += kSelectThreads) {
     const int j = base + threadIdx.x;
     bool take = j < n && (j < j0 || j >= j1), equal = false;
@@ -442,6 +446,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   const int n = bad ? 0 : (L + kBlockSize - 1) / kBlockSize;   // a bad length: an empty list
   if (n <= K) {
     if (bad && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
+#pragma unroll 1
     for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < n ? i : -1;
     return;
   }
@@ -451,6 +456,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- range and error of the fp32 scores; NaN marks the blocks that are in doubt anyway
   float top = -INFINITY, low = INFINITY, err = 0.f, odd = 0.f;
+#pragma unroll 4
   for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
     const float2 x = approx[j];
     const bool fine = x.y < INFINITY;
@@ -463,6 +469,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
       odd = 1.f;
     }
   }
+#pragma unroll 1
   for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) u.hist[i] = 0;
   if (threadIdx.x == 0) {
     num_doubt = num_in = 0;
@@ -483,6 +490,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   auto bin = [&](float x) { return min(kSelectBins - 1, static_cast<int>((x - low) * scale)); };   // grows with x
   float t0 = -INFINITY, t1 = INFINITY;   // no block with a finite score: all are in doubt
   if (need > 0) {
+#pragma unroll 1
     for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
       const float x = score(j);
       if (x == x) atomicAdd(&u.hist[bin(x)], 1);
@@ -504,6 +512,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     const int at = found[0];
     float a = INFINITY, z = -INFINITY;
     if (at >= 0) {
+#pragma unroll 1
       for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
         const float x = score(j);
         if (x == x && bin(x) == at) {
@@ -519,9 +528,11 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   __syncthreads();
   // ---- chosen, not chosen, in doubt.  (Blocks without a finite fp32 score may be above any other
   // and take its place: with some, nothing is certain to be chosen; what is below t0 is still out.)
+#pragma unroll 1
   for (int i = threadIdx.x; i < kSelectMaxBlocks / 32 && i * 32 < n; i += kSelectThreads) u.bits[i] = 0u;
   __syncthreads();
   const bool fast = n <= kSelectMaxBlocks;
+#pragma unroll 1
   for (int base = j0; base < j1 && need > 0 && fast; base += kSelectThreads) {
     const int j = base + threadIdx.x;
     const float x = j < j1 ? score(j) : -INFINITY;
@@ -546,31 +557,38 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     return;
   }
   if (!fast) {   // need == 0: the first and last blocks alone
+#pragma unroll 1
     for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < j0 ? i : n - K + i;
     return;
   }
   if (m > left) {
+#pragma unroll 1
     for (int i = warp; i < m; i += kSelectWarps) {
       const unsigned long long key = exact_key<T, G>(p, b, g, doubt_j[i]);
       if (lane == 0) doubt_key[i] = key;
     }
     __syncthreads();
   }
+#pragma unroll 1
   for (int i = threadIdx.x; i < m; i += kSelectThreads) {
     const int j = doubt_j[i];
     int before = 0;   // blocks in doubt that are chosen before this one
     if (m > left) {
       const unsigned long long key = doubt_key[i];
+#pragma unroll 1
       for (int k = 0; k < m; ++k) before += doubt_key[k] > key || (doubt_key[k] == key && doubt_j[k] < j);
     }
     if (before < left) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
   }
+#pragma unroll 1
   for (int j = threadIdx.x; j < j0; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+#pragma unroll 1
   for (int j = j1 + threadIdx.x; j < n; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
   __syncthreads();
   // ---- the list
   int written = 0;
   const int words = (n + 31) / 32;
+#pragma unroll 1
   for (int base = 0; base < words; base += kSelectThreads) {
     unsigned w = base + threadIdx.x < words ? u.bits[base + threadIdx.x] : 0u;
     int total;
