@@ -1070,27 +1070,29 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
       }
       pdl_wait();   // the prefix's partials are visible from here on
       const int na = prefix_partials<G>(p, group, b, hh);
-      const float M_own = M;
-      for (int k = 0; k < na; ++k) M = fmaxf(M, p.ws_m[at + k * pitch]);
-      const float f = M_own == -INFINITY && lsum == 0.f ? 0.f : ex2(M_own - M);
-      lsum *= f;
-      a.x *= f;
-      a.y *= f;
-      a.z *= f;
-      a.w *= f;
       for (int k0 = 0; k0 < na; k0 += kJoinBatch) {
         float mk[kJoinBatch], lk[kJoinBatch];
         float4 x[kJoinBatch];
 #pragma unroll
         for (int u = 0; u < kJoinBatch; ++u) {   // every load of the batch in flight
           const size_t row = at + min(k0 + u, na - 1) * pitch;
-          mk[u] = p.ws_m[row];
+          mk[u] = k0 + u < na ? p.ws_m[row] : -INFINITY;
           lk[u] = k0 + u < na ? p.ws_l[row] : 0.f;
           x[u] = *reinterpret_cast<const float4 *>(p.ws_o + row * D + d);
         }
+        float m_new = M;
+#pragma unroll
+        for (int u = 0; u < kJoinBatch; ++u) m_new = fmaxf(m_new, mk[u]);
+        const float f = M == -INFINITY && lsum == 0.f ? 0.f : ex2(M - m_new);
+        M = m_new;
+        lsum *= f;
+        a.x *= f;
+        a.y *= f;
+        a.z *= f;
+        a.w *= f;
 #pragma unroll
         for (int u = 0; u < kJoinBatch; ++u) {
-          if (k0 + u >= na || (mk[u] == -INFINITY && lk[u] == 0.f)) continue;   // no token: o may be anything
+          if (mk[u] == -INFINITY && lk[u] == 0.f) continue;   // past the end, or no token: o may be anything
           const float fk = ex2(mk[u] - M);
           lsum += fk * lk[u];
           a.x += fk * x[u].x;

@@ -258,14 +258,14 @@ __device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int
 }
 
 template <typename T, int G>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 8) block_score_kernel(const SelectParams p) {
   pdl_wait();
   pdl_trigger();
-  int item = blockIdx.x;
-  const int chunk = item % p.chunks;
-  item /= p.chunks;
+  int item = blockIdx.x;   // the heads of the same blocks side by side: their rows are neighbours in memory
   const int g = item % p.num_kv_heads;
-  const int b = item / p.num_kv_heads;
+  item /= p.num_kv_heads;
+  const int chunk = item % p.chunks;
+  const int b = item / p.chunks;
   const int L = p.context_lens[b];
   if (L < 0 || L > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize) {
     if (chunk == 0 && g == 0 && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
