@@ -363,7 +363,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
  *               aligned; scratch.  Calls that overlap on the GPU need one each.
  * dtype PA_F16 or PA_BF16, head_dim 128, group size (num_heads / num_kv_heads) 1,
  * 2, 4 or 8.  Accumulation is fp32; softmax weights enter the prefix's P V as
- * fp16 (relative rounding 2^-11, PA_F16) or as two bf16 parts (2^-17, PA_BF16).
+ * fp16 (relative rounding 2^-11, PA_F16) or as two bf16 parts (2^-15, PA_BF16).
  * Bad block ids of a prefix read as zeros (PA_DEV_BAD_BLOCK_ID).
  * Errors: as pa_decode, PA_ERR_DTYPE for other types, PA_ERR_SHAPE also for
  * num_seqs > 0 without groups and a max_prefix_len off 16.

@@ -1015,13 +1015,13 @@ pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, cons
   // the new tokens may start anywhere in a block: n tokens touch at most ceil((n + 15) / 16) blocks
   p.blocks_per_seq = (int)(((long long)max_new_len + 2 * kBlockSize - 2) / kBlockSize);
   const long long total = (long long)num_seqs * p.blocks_per_seq * p.chunks_per_token;
-  long long ctas = (total + 127) / 128;
+  long long ctas = (total + 255) / 256;
   if (ctas > 64LL * sm_count()) ctas = 64LL * sm_count();
   cudaStream_t s = (cudaStream_t)stream;
   switch (dtype) {
-    case PA_F32: return launch(pa::block_bounds_kernel<float>, dim3((unsigned)ctas), dim3(128), 0, s, p);
-    case PA_F16: return launch(pa::block_bounds_kernel<__half>, dim3((unsigned)ctas), dim3(128), 0, s, p);
-    case PA_BF16: return launch(pa::block_bounds_kernel<__nv_bfloat16>, dim3((unsigned)ctas), dim3(128), 0, s, p);
+    case PA_F32: return launch(pa::block_bounds_kernel<float>, dim3((unsigned)ctas), dim3(256), 0, s, p);
+    case PA_F16: return launch(pa::block_bounds_kernel<__half>, dim3((unsigned)ctas), dim3(256), 0, s, p);
+    case PA_BF16: return launch(pa::block_bounds_kernel<__nv_bfloat16>, dim3((unsigned)ctas), dim3(256), 0, s, p);
     case PA_FP8_E4M3: break;
   }
   return PA_ERR_DTYPE;

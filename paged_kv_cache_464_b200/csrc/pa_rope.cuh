@@ -11,6 +11,11 @@
 // Every product and sum is fp32, each rounded by itself (no contraction: the
 // result does not depend on which of the two products the compiler would fuse),
 // and the row is rounded once to its stored type.
+//
+// Bound by HBM: 8192 tokens of 32/8 bf16 heads (206 MB) take 32.5 us, 97% of the copy
+// bandwidth.  E4M3 caches: 4093 tokens (92 MB) 22.9 us, 62%, where the IEEE quotients by the
+// scale cost 3 us (multiplying instead: 19.9); checking a product for a nearby tie
+// and dividing only then was slower (24.4; a row at a time 28.7).
 #pragma once
 
 #include "pa_common.cuh"

@@ -57,9 +57,10 @@ __device__ __forceinline__ void bound_chunk(uint4 &a, const uint4 &b) {
 // The bounds of every block that holds one of a sequence's last new_lens[b]
 // tokens, from all of the block's tokens (those before the new ones too, so
 // the result does not depend on what the bounds held).  A thread owns one 16-byte
-// chunk of one head's row and loads it for the block's 16 tokens at once.
+// chunk of one head's row and loads it for the block's 16 tokens at once.  528 blocks of
+// 8 heads (19 MB) take 3.6 us, 256 blocks 2.8 (a launch and three dependent loads).
 template <typename T>
-__global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsParams p) {
   pdl_wait();
   pdl_trigger();
   const long long per_seq = static_cast<long long>(p.blocks_per_seq) * p.chunks_per_token;
@@ -104,8 +105,9 @@ __global__ void __launch_bounds__(128) block_bounds_kernel(const BoundsParams p)
 // Which blocks are chosen is decided by fp64 scores, but few of them are computed:
 // block_score_kernel gives every block an fp32 score with a bound on its error, and
 // block_select_kernel computes fp64 scores only for the blocks that the bound leaves in
-// doubt.  fp64 scores of all blocks cost 80 us for 8 x 8 x 2048 blocks and 8 heads
-// (two conversions to fp64 for each product, 16 a cycle and SM), against 17.
+// doubt.  fp64 scores of all blocks cost 80 us for 8 x 8 x 2048 blocks and 8 heads (two
+// conversions to fp64 for each product, 16 a cycle and SM), the fp32 ones 16 (67 MB at
+// 4.2 TB/s, 64% of the copy bandwidth: each warp's chain of length, block id and rows).
 struct SelectParams {
   const void *q;                  // [S][Hq][D]
   const uint4 *bounds;            // [NB][2][Hkv][16 chunks]
@@ -420,7 +422,12 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
 // With E the largest error bound and the need-th largest fp32 score within [t0, t1]
 // (the scores of its bin of an even histogram), the need-th largest score is within
 // [t0 - E, t1 + E]: an fp32 score above t1 + 2 E is chosen, one below t0 - 2 E is not,
-// and only the rest is in doubt and ranked by fp64 scores.
+// and only the rest is in doubt and ranked by fp64 scores (one to three blocks for N(0, 1)
+// data; if more than kSelectDoubt, or more blocks than kSelectMaxBlocks, select_all_exact
+// decides).  9 us for 8 CTAs of 2048 blocks, 10 for 64: its length is a dozen
+// block-wide steps of 500 to 2000 cycles whose code runs once.  Bisection in
+// registers in the histogram's place was as long (13300 cycles against 14400) and slower
+// for 488 CTAs; 256 threads are slower for few CTAs (19.8 against 18.5 a pass).
 template <typename T, int G>
 __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const SelectParams p) {
   __shared__ union {

@@ -7,7 +7,9 @@ import torch
 import step_reference as ref
 
 pytestmark = pytest.mark.gpu
-P_BITS = {"f16": 11, "bf16": 16}     # the prefix's softmax weights: one fp16 part, two bf16 parts
+# The prefix's softmax weights: one fp16 part (half a step, 2^-11), or two bf16 parts: the upper 16 bits leave less
+# than 2^-7 of the weight, which is rounded to bf16 (2^-8 of that): 2^-15.
+P_BITS = {"f16": 11, "bf16": 15}
 
 
 @pytest.fixture(scope="module")
