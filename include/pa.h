@@ -151,8 +151,8 @@ pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, doub
  *               likewise with num_kv_heads; q_out likewise.  All in dtype.
  *               q_out may be q itself (same pointer and stride: rotated in
  *               place); otherwise it must not overlap q, key or value.
- * positions     [num_tokens] int64.  A token with position < 0 is padding: none
- *               of its rows is read or written.  position >= max_position: the
+ * positions     [num_tokens] int64.  A token with position < 0 is padding: its
+ *               rows may be read, and nothing is written for it.  position >= max_position: the
  *               token is skipped and recorded as PA_DEV_BAD_POSITION.
  * cos_sin       [max_position][rotary_dim] fp32 (pa_rope_table, or the caller's).
  * slot_mapping  [num_tokens] int64 as in pa_reshape_and_cache: slot < 0 writes no
@@ -165,7 +165,8 @@ pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, doub
  * Elements from rotary_dim on, and V, are copied bit for bit.
  * Errors: PA_ERR_NULL, PA_ERR_DTYPE, PA_ERR_SHAPE (as pa_reshape_and_cache;
  * rotary_dim not a multiple of 16 (fp32: 8) or > head_dim; a stride below the
- * row or above 2^31 - 1; max_position <= 0; q_out overlapping), PA_ERR_ALIGN (16
+ * row or above 2^31 - 1; max_position <= 0; num_heads <= 0; more than 65536
+ * heads; q_out overlapping), PA_ERR_ALIGN (16
  * bytes for every tensor but positions and slot_mapping (8), strides multiples
  * of 16 bytes), PA_ERR_CUDA.  num_tokens == 0 is a no-op.
  */
@@ -366,7 +367,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
  * fp16 (relative rounding 2^-11, PA_F16) or as two bf16 parts (2^-15, PA_BF16).
  * Bad block ids of a prefix read as zeros (PA_DEV_BAD_BLOCK_ID).
  * Errors: as pa_decode, PA_ERR_DTYPE for other types, PA_ERR_SHAPE also for
- * num_seqs > 0 without groups and a max_prefix_len off 16.
+ * num_seqs > 0 without groups, a max_prefix_len off 16 and more than 2^31 - 1 CTAs.
  */
 pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
                                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
@@ -414,11 +415,14 @@ size_t pa_select_blocks_workspace_bytes(int num_seqs, int num_kv_heads, int max_
  *
  * selected      [num_seqs][num_kv_heads][num_selected] int32 (written): logical
  *               block indices in ascending order, -1 behind them when n <
- *               num_selected.  A bad context length gives a list of -1.
+ *               num_selected.  A bad context length gives a list of -1; a block
+ *               whose table entry is bad (PA_DEV_BAD_BLOCK_ID) ranks last.
  * block_bounds  as pa_update_block_bounds left them for every block of the context.
  * max_context_len  host-side upper bound of context_lens.
+ * workspace     pa_select_blocks_workspace_bytes(...) bytes, 256-byte aligned;
+ *               scratch.  Calls that overlap on the GPU need one each.
  * Errors: PA_ERR_NULL, PA_ERR_DTYPE, PA_ERR_SHAPE (as pa_decode; num_selected <=
- * 0; sink_blocks + recent_blocks > num_selected), PA_ERR_WORKSPACE, PA_ERR_ALIGN,
+ * 0 or > 2^26; sink_blocks + recent_blocks > num_selected), PA_ERR_WORKSPACE, PA_ERR_ALIGN,
  * PA_ERR_CUDA.
  */
 pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block_bounds, const int32_t *block_tables,
@@ -443,6 +447,9 @@ size_t pa_decode_selected_workspace_bytes(int num_seqs, int num_heads, int num_k
  *               PA_DEV_BAD_BLOCK_ID (detail = the entry), a bad table entry
  *               likewise (detail = the id).
  * A row whose list names no block is all zeros.  dtype PA_F32, PA_F16 or PA_BF16.
+ * workspace     pa_decode_selected_workspace_bytes(...) bytes, 256-byte aligned;
+ *               scratch.  Calls that overlap on the GPU need one each.
+ * PA_ERR_SHAPE also for num_selected <= 0 or > 2^26.
  * Other arguments, results and errors as pa_decode.
  */
 pa_status_t pa_decode_selected(void *out, const void *q, const void *k_cache, const void *v_cache,

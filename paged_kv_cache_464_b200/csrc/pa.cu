@@ -674,7 +674,7 @@ pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, doub
 
 namespace {
 
-// Do the byte ranges of two sets of rows (first address, rows, stride, row bytes) overlap?
+// Do two byte ranges overlap?
 bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
@@ -870,20 +870,18 @@ pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa
     auto kernel = pa::pa_shared_prefix_kernel<T, G>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::PrefixSmem::kAlloc) != cudaSuccess)
       return PA_ERR_CUDA;
-    const long long grid = (long long)num_groups * p.row_ctas * p.num_kv_heads * p.parts;
-    if (grid > INT32_MAX) return PA_ERR_SHAPE;
-    st = launch(kernel, dim3((unsigned)grid), dim3(pa::kPrefixThreads), pa::PrefixSmem::kAlloc, stream, mk, mv, p);
+    const unsigned grid = (unsigned)(num_groups * p.row_ctas * p.num_kv_heads * p.parts);
+    st = launch(kernel, dim3(grid), dim3(pa::kPrefixThreads), pa::PrefixSmem::kAlloc, stream, mk, mv, p);
     if (st != PA_OK) return st;
   }
   using SM = pa::DecodeSmem<T, G, Math>;
   auto suffix = pa::pa_decode_partition_kernel<T, G, Math, pa::kDecodeWarps, pa::kWalkSuffix>;
   if (cudaFuncSetAttribute(suffix, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc) != cudaSuccess)
     return PA_ERR_CUDA;
-  const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.max_partitions;
-  if (grid > INT32_MAX) return PA_ERR_SHAPE;
+  const unsigned grid = (unsigned)(p.num_seqs * p.num_kv_heads * p.max_partitions);
   pa::SuffixParams sp = p;
   sp.stall_cta = 0;
-  st = launch(suffix, dim3((unsigned)grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, sp);
+  st = launch(suffix, dim3(grid), dim3(pa::kDecodeThreads), SM::kAlloc, stream, mk, mv, sp);
   if (st != PA_OK || p.max_partitions == 1) return st;
   const long long rows = (long long)p.num_seqs * p.num_heads;
   long long ctas = (rows + pa::kReduceWarps - 1) / pa::kReduceWarps;
@@ -942,6 +940,10 @@ pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cach
     return PA_ERR_ALIGN;
   const PrefixPlan plan = plan_prefix(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len,
                                       max_suffix_len, max_group_size);
+  // CTAs of the two launches (in floating point: a product of four counts may pass 2^63)
+  if ((double)num_groups * plan.row_ctas * num_kv_heads * plan.parts > INT32_MAX ||
+      (double)num_seqs * num_kv_heads * plan.suffix_parts > INT32_MAX)
+    return PA_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.ws.bytes) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
   CUtensorMap mk, mv;
@@ -1014,6 +1016,7 @@ pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, cons
   p.max_new_len = max_new_len;
   // the new tokens may start anywhere in a block: n tokens touch at most ceil((n + 15) / 16) blocks
   p.blocks_per_seq = (int)(((long long)max_new_len + 2 * kBlockSize - 2) / kBlockSize);
+  if (p.blocks_per_seq > max_blocks_per_seq) p.blocks_per_seq = max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
   const long long total = (long long)num_seqs * p.blocks_per_seq * p.chunks_per_token;
   long long ctas = (total + 255) / 256;
   if (ctas > 64LL * sm_count()) ctas = 64LL * sm_count();
@@ -1030,6 +1033,8 @@ pa_status_t pa_update_block_bounds(const void *k_cache, void *block_bounds, cons
 }  // extern "C"
 
 namespace {
+
+constexpr int kMaxSelected = 1 << 26;   // blocks of a list: its tokens are counted in 32 bits
 
 template <typename T, int G>
 pa_status_t launch_choice(const pa::SelectParams &p, cudaStream_t s) {
@@ -1076,7 +1081,7 @@ pa_status_t pa_select_blocks(int32_t *selected, const void *q, const void *block
   if (num_seqs < 0 || num_heads <= 0 || num_heads % num_kv_heads != 0 || max_context_len < 0 ||
       max_blocks_per_seq < 0 || (long long)max_blocks_per_seq * kBlockSize > INT32_MAX || num_selected <= 0 ||
       sink_blocks < 0 || recent_blocks < 0 || (long long)sink_blocks + recent_blocks > num_selected ||
-      num_selected > (1 << 27))
+      num_selected > kMaxSelected)
     return PA_ERR_SHAPE;
   const int group = num_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_SHAPE;
@@ -1202,7 +1207,7 @@ extern "C" {
 size_t pa_decode_selected_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                           int num_selected) {
   if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_selected <= 0 ||
-      num_selected > (1 << 27))
+      num_selected > kMaxSelected)
     return 0;
   return selected_workspace(num_seqs, num_heads, num_kv_heads, head_dim, num_selected).bytes;
 }
@@ -1213,7 +1218,7 @@ pa_status_t pa_decode_selected(void *out, const void *q, const void *k_cache, co
                                void *workspace, size_t workspace_bytes, int64_t num_blocks, int block_size,
                                int num_kv_heads, int head_dim, pa_dtype_t dtype, void *stream) {
   if (dtype == PA_FP8_E4M3) return PA_ERR_DTYPE;
-  if (num_selected <= 0 || num_selected > (1 << 27)) return PA_ERR_SHAPE;
+  if (num_selected <= 0 || num_selected > kMaxSelected) return PA_ERR_SHAPE;
   if (num_seqs > 0 && !selected) return PA_ERR_NULL;
   if (!aligned(selected, 4)) return PA_ERR_ALIGN;
   // every other check is pa_decode's (one partition: the split is planned below)

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsParams p)
       continue;
     }
     const int j = (L - n) / kBlockSize + i;
-    if (n == 0 || j * kBlockSize >= L) continue;
+    if (n == 0 || j > (L - 1) / kBlockSize) continue;   // (j * 16 may pass 2^31)
     const int id = p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j];
     if (id < 0 || id >= p.num_blocks) {
       if (c == 0) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
@@ -113,7 +113,7 @@ struct SelectParams {
   const uint4 *bounds;            // [NB][2][Hkv][16 chunks]
   const int32_t *block_tables;    // [S][MBS]
   const int32_t *context_lens;    // [S]
-  float2 *approx;                 // [S][Hkv][max_blocks] (score, error bound; not finite: in doubt)
+  float2 *approx;                 // [S][Hkv][max_blocks] (score, error bound; an infinite bound: in doubt)
   unsigned long long *keys;       // [S][Hkv][max_blocks] fp64 scores in an order-preserving code
   int32_t *selected;              // [S][Hkv][K]
   long long num_blocks;
@@ -136,7 +136,8 @@ constexpr int kScoreBlocks = 64;   // blocks a CTA scores: 16 a warp
 // 16-bit values are exact; a sum of 256 of them in fp32, whatever its order and if each
 // step drops bits below 2^-23 of the larger operand, is off by less than 2^-15 of
 // the sum of magnitudes; 64 fp32 products and sums by less than 2^-17.
-constexpr float kScoreError = 1.f / 16384;
+// Products and sums below the fp32 range lose at most 2^-126 each.
+constexpr float kScoreError = 1.f / 16384, kScoreErrorMin = 0x1p-116f;
 
 // 16-bit caches: s_h(j) = q+ . hi + q- . lo with q+ = max(q, 0), q- = min(q, 0), as
 // warp-level matrix products (m16n8k16): 16 blocks by 8 heads, head_dim in any
@@ -161,9 +162,11 @@ __device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, 
   }
   const size_t hi_off = static_cast<size_t>(p.num_kv_heads) * kChunksPerRow;
   uint4 lo[2][4], hi[2][4];
+  bool bad[2];   // no such block: left to the fp64 score, which puts it last
 #pragma unroll
   for (int r = 0; r < 2; ++r) {   // rows gid, gid + 8
     const int rid = __shfl_sync(kFullMask, id, gid + 8 * r);
+    bad[r] = rid < 0;
     const uint4 *src = p.bounds + (static_cast<size_t>(rid < 0 ? 0 : rid) * 2 * p.num_kv_heads + g) * kChunksPerRow + tig;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -196,7 +199,7 @@ __device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, 
 #pragma unroll
   for (int r = 0; r < 2; ++r) {   // s[2r], s[2r + 1]: row gid + 8 r, heads 2 tig, 2 tig + 1
     float best = -INFINITY, most = 0.f;
-    bool odd = false;   // not finite
+    bool odd = bad[r];   // or not finite
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * tig + e >= G) continue;
@@ -211,7 +214,7 @@ __device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, 
       odd = __shfl_xor_sync(kFullMask, odd ? 1 : 0, off) != 0 || odd;
     }
     const int j = j0 + gid + 8 * r;
-    if (tig == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : most * kScoreError);
+    if (tig == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : fmaf(most, kScoreError, kScoreErrorMin));
   }
 }
 
@@ -228,7 +231,8 @@ __device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int
   for (int i = 0; i < 8; ++i) {
     const int j = j0 + 2 * i + (lane >> 4);
     int id = j < n ? p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + j] : 0;
-    if (id < 0 || id >= p.num_blocks) {
+    const bool bad = id < 0 || id >= p.num_blocks;   // left to the fp64 score, which puts it last
+    if (bad) {
       if (c == 0) record_error(1 /*PA_DEV_BAD_BLOCK_ID*/, id);
       id = 0;
     }
@@ -237,7 +241,7 @@ __device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int
     Elem<float>::unpack(src[0], lo);
     Elem<float>::unpack(src[static_cast<size_t>(p.num_kv_heads) * kChunksPerRow], hi);
     float best = -INFINITY, most = 0.f;
-    bool odd = false;
+    bool odd = bad;
 #pragma unroll
     for (int h = 0; h < G; ++h) {
       float s = 0.f, t = 0.f;
@@ -255,7 +259,7 @@ __device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int
       best = fmaxf(best, s);
       most = fmaxf(most, t);
     }
-    if (c == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : most * kScoreError);
+    if (c == 0 && j < n) out[j] = make_float2(best, odd ? INFINITY : fmaf(most, kScoreError, kScoreErrorMin));
   }
 }
 

@@ -42,6 +42,19 @@ def test_bounds(pa, ty, hkv, new):
     assert torch.equal(bd2, bd)
 
 
+@pytest.mark.parametrize("most", [1000, 1 << 30, (1 << 31) - 1])
+def test_bounds_with_a_generous_maximum(pa, most):
+    """Only an upper bound: the rows' last blocks are found all the same."""
+    k, _, tables, lens = ref.make_cache(LENS, 2, "bf16", seed=6)
+    n = lens.clamp(max=1)
+    bounds = torch.full((k.shape[0], 2, 2, 128), 9.0, dtype=k.dtype)
+    kd, bd, td, ld, nd = cuda(k, bounds, tables, lens, n)
+    pa.update_block_bounds(kd, bd, td, ld, nd, max_new_len=most)
+    assert torch.equal(bd.cpu(), ref.block_bounds(k, bounds, tables, lens, n))
+    none = torch.empty((len(LENS), 0), dtype=torch.int32, device="cuda")     # no table, no token
+    pa.update_block_bounds(kd, bd, none, torch.zeros_like(ld), torch.zeros_like(nd), max_new_len=most)
+
+
 def test_bounds_keep_nan_and_infinity(pa):
     k, _, tables, lens = ref.make_cache([40], 2, "bf16", seed=1)
     k[tables[0, 0], 3, 0, 5] = float("nan")
@@ -178,6 +191,37 @@ def test_choice_with_scores_that_overflow_fp32(pa):
         want = ref.choose(q, bounds, tables, lens, K, 0, 1)
         got = pa.select_blocks(*cuda(q, bounds, tables, lens), K, sink_blocks=0, recent_blocks=1)
         assert torch.equal(got.cpu(), want), K
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+def test_choice_with_scores_below_fp32(pa, ty):
+    """Products under the smallest fp32 number (f16: its subnormals): the order is still that of the 64-bit scores."""
+    n, d = 200, ref.HEAD_DIM[ty]
+    lens = torch.tensor([n * 16], dtype=torch.int32)
+    tables = torch.arange(n, dtype=torch.int32)[None]
+    g = torch.Generator().manual_seed(12)
+    small = 2.0 ** -20 if ty == "f16" else 2.0 ** -80
+    bounds = (torch.randn((n, 2, 1, d), generator=g) * small).to(ref.TYPES[ty])
+    bounds = torch.stack([bounds.amin(1), bounds.amax(1)], 1)
+    q = (torch.randn((1, 4, d), generator=g) * small).to(ref.TYPES[ty])
+    for K in (1, 8, 77):
+        want = ref.choose(q, bounds, tables, lens, K, 0, 1)
+        got = pa.select_blocks(*cuda(q, bounds, tables, lens), K, sink_blocks=0, recent_blocks=1)
+        assert torch.equal(got.cpu(), want), K
+
+
+@pytest.mark.expects_device_error
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+def test_choice_puts_bad_blocks_last(pa, ty):
+    k, _, tables, lens = ref.make_cache([640], 1, ty, seed=4)
+    bounds = bounds_of(k, tables, lens)
+    bounds[0] = bounds.abs().nan_to_num(1.0).amax() * torch.tensor([-1.0, 1.0])[:, None, None].to(bounds.dtype)   # block 0 above all
+    q = ref.make_q(1, 4, ty, seed=1)
+    t = tables.clone()
+    t[0, 7], t[0, 21] = -7, k.shape[0]
+    got = pa.select_blocks(*cuda(q, bounds, t, lens), 38, sink_blocks=0, recent_blocks=0).cpu()
+    assert pa.get_device_error(clear=True)[0] == 1
+    assert got[0, 0].tolist() == [j for j in range(40) if j not in (7, 21)]
 
 
 @pytest.mark.expects_device_error

@@ -86,6 +86,8 @@ def test_shared_prefix_refusals(capi):
     assert f(mp=-16) == SHAPE and f(mp=500) == SHAPE and f(ms=-1) == SHAPE
     assert f(mbs=-1) == SHAPE and f(mbs=1 << 28) == SHAPE
     assert f(scale=0.0) == SHAPE and f(scale=-1.0) == SHAPE and f(scale=float("nan")) == SHAPE
+    assert f(n=(1 << 31) - 1, mg=1 << 24, Hq=1 << 19, Hkv=1 << 16) == SHAPE   # a grid past 2^63
+    assert f(S=1 << 20, Hq=1 << 14, Hkv=1 << 14) == SHAPE
     for name in ("out", "q", "kc", "vc", "bt", "cl", "gs", "pl"):
         assert f(**{name: None}) == NULL, name
     for name in ("out", "q", "kc", "vc"):
@@ -140,6 +142,7 @@ def test_select_blocks_refusals(capi):
     assert f(S=0) == 0
     assert f(dt=FP8) == DTYPE and f(dt=7) == DTYPE and f(D=64) == SHAPE
     assert f(K=0) == SHAPE and f(K=-1) == SHAPE and f(sink=-1) == SHAPE and f(rec=-1) == SHAPE
+    assert f(K=(1 << 26) + 1) == SHAPE
     assert f(sink=3, rec=2) == SHAPE and f(ml=-1) == SHAPE and f(Hq=6) == SHAPE and f(Hq=7) == SHAPE
     for name in ("sel", "q", "bb", "bt", "cl"):
         assert f(**{name: None}) == NULL, name
@@ -163,6 +166,7 @@ def test_decode_selected_refusals(capi):
         return _selected(capi, **k)
     assert f(S=0) == 0
     assert f(dt=FP8) == DTYPE and f(dt=7) == DTYPE and f(D=64) == SHAPE
+    assert f(K=(1 << 26) + 1) == SHAPE and capi.decode_selected_workspace_bytes(2, 8, 2, 128, (1 << 26) + 1) == 0
     assert f(K=0) == SHAPE and f(K=-3) == SHAPE and f(Hq=6) == SHAPE and f(S=-1) == SHAPE
     assert f(scale=float("inf")) == SHAPE and f(mbs=-1) == SHAPE and f(mbs=1 << 28) == SHAPE
     for name in ("out", "q", "kc", "vc", "bt", "cl", "sel"):
