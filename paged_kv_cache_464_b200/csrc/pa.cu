@@ -809,9 +809,10 @@ struct PrefixPlan {
 // CTA (one an SM) takes 8.5 of set-up and epilogue and 2.9 a step; a step is a
 // tile, or two where a CTA has at most 128 rows.  A last wave that is not full counts for
 // at least half.  Each partition's partials cost 0.35 to combine and their
-// bytes, written and read.  (47 sequences in three groups, 32 KV heads: 45.2 a call with
-// the two partitions chosen, 57.1 with one, 54.5 with three; 128 sequences over 1024 tokens:
-// 41.0 with four, 41.7 with eight; 5 over 4000: 18.2 with eight, 19.2 with sixteen.)
+// bytes, written and read.  (47 sequences in three groups, 32 KV heads: 42.6 a call with
+// the two partitions chosen, 52.5 with one, 51.2 with three; 128 sequences over 1024 tokens:
+// 38.0 with four, 39.2 with three, 39.5 with eight; 5 over 4000: 15.9 with eight, 16.5 with
+// sixteen, 24.6 with three.)
 PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_prefix_len,
                        int max_suffix_len, int max_group_size) {
   PrefixPlan r{};
@@ -1159,8 +1160,8 @@ pa_status_t launch_selected(const CUtensorMap &mk, const CUtensorMap &mv, const 
   const long long grid = (long long)p.num_seqs * p.num_kv_heads * p.max_partitions;
   if (grid > INT32_MAX) return PA_ERR_SHAPE;
   // More CTAs than a wave of three an SM: two-warp CTAs, six an SM, where the block
-  // math has them (61 sequences x 8 heads of 33 blocks: 62.1 us a pass of choice and
-  // decode against 67.9; within one wave four warps are faster, 19.1 against 20.4 at 64 CTAs).
+  // math has them (640 CTAs of 16 blocks, G = 4: 19.5 us against 21.7 with four warps, 768 CTAs 17.6
+  // against 19.2; within one wave four warps: 64 CTAs 7.6 against 8.8, 384 CTAs 17.1 against 17.7).
   if constexpr (W == pa::kDecodeWarps && !Math::kNeedsQInSmem) {
     if (grid > 3LL * sm_count()) return launch_selected<T, G, Math, 2>(mk, mv, p, stream);
   }
