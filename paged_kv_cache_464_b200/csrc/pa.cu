@@ -751,8 +751,13 @@ pa_status_t rope_impl(void *q_out, const void *q, const void *key, const void *v
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.rotary = rotary_dim;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
+  auto split = [](float scale) {
+    const float unit = scale < 0x1p-60f ? 0x1p96f : scale > 0x1p60f ? 0x1p-64f : 1.f;
+    const float s = scale * unit;   // exact
+    return pa::E4m3Scale{s, 1.f / s, unit};
+  };
+  p.k_scale = split(k_scale);
+  p.v_scale = split(v_scale);
   const bool fp8 = cache_dtype == PA_FP8_E4M3;
   cudaStream_t s = (cudaStream_t)stream;
   switch (dtype) {

@@ -13,9 +13,8 @@
 // and the row is rounded once to its stored type.
 //
 // Bound by HBM: 8192 tokens of 32/8 bf16 heads (206 MB) take 32.5 us, 97% of the copy
-// bandwidth.  E4M3 caches: 4093 tokens (92 MB) 22.9 us, 62%, where the IEEE quotients by the
-// scale cost 3 us (multiplying instead: 19.9); checking a product for a nearby tie
-// and dividing only then was slower (24.4; a row at a time 28.7).
+// bandwidth.  E4M3 caches: 4093 tokens (92 MB) 19.4 us, 73%: half the time the SMs issue
+// (rotation, quotients by the scale, conversions), and 3.5 waves of CTAs leave a tail.
 #pragma once
 
 #include "pa_common.cuh"
@@ -42,6 +41,12 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ cos
   }
 }
 
+// A 1-byte cache's scale as power * s with s in [2^-60, 2^64] and power a power of two, so that
+// remainders of quotients by s are exact; inv = 1 / s rounded to nearest.
+struct E4m3Scale {
+  float s, inv, unit;   // unit = 1 / power
+};
+
 struct RopeParams {
   void *q_out;                      // [T] rows of Hq * D elements, q_out_stride apart
   const void *q, *key, *value;      // [T] rows, *_stride elements apart; heads contiguous in a row
@@ -52,7 +57,7 @@ struct RopeParams {
   long long q_out_stride, q_stride, k_stride, v_stride;   // in elements
   long long num_slots, max_position;
   int num_tokens, num_heads, num_kv_heads, rotary;
-  float k_scale, v_scale;           // 1-byte caches
+  E4m3Scale k_scale, v_scale;       // 1-byte caches
 };
 
 // Two 16-byte chunks of fp32 values -> where they go: T rows (16 bytes a chunk)
@@ -84,12 +89,30 @@ __device__ __forceinline__ uint4 pack_chunk<__half>(const float *f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint2 pack_e4m3(const float *f, float scale) {
+// The quotient by a scale, rounded to fp32, where it is between 2^-12 and 512; below and
+// above, a number with the same E4M3 code.  Two corrections by the remainder: x * inv is
+// off by up to 1.5 units of the last place, the first correction by less than one, and a
+// quotient within one becomes the rounded quotient by another (Markstein, Computation of elementary
+// functions on the IBM RISC System/6000 processor, IBM J. Res. Dev. 34, 1990).  x * unit is exact
+// or too small or large to matter; the remainder's sign keeps -0.  19.4 us for the case above
+// against 22.7 with IEEE divisions, whose branches cost more than their instructions.
+__device__ __forceinline__ float e4m3_quotient(float x, const E4m3Scale &c) {
+  x *= c.unit;
+  const float q = x * c.inv;
+  const float y = fmaf(-fmaf(q, c.s, -x), c.inv, q);
+  const float z = fmaf(-fmaf(y, c.s, -x), c.inv, y);
+  return fabsf(q) < 512.f ? z : q;   // q itself: saturates, infinity, NaN
+}
+
+__device__ __forceinline__ uint2 pack_e4m3(const float *f, const E4m3Scale &scale) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = e4m3_quotient(f[i], scale);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint16_t a;   // cvt packs its first source into the upper byte
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(f[2 * i + 1] / scale), "f"(f[2 * i] / scale));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
     w[i] = a;
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
@@ -188,7 +211,7 @@ __global__ void __launch_bounds__(kRopeTokens * kRopeHeads * kRopeItems) rope_an
       }
     }
     if (kFp8 && !is_q) {
-      const float scale = is_k ? p.k_scale : p.v_scale;
+      const E4m3Scale scale = is_k ? p.k_scale : p.v_scale;
       uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) +
                    (slot * p.num_kv_heads + hl) * kChunksPerRow;
       const uint2 y0 = pack_e4m3(f0, scale), y1 = pack_e4m3(f1, scale);

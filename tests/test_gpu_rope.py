@@ -110,6 +110,54 @@ def test_fp8_cache(pa, ty, interleaved, part):
     assert torch.equal(q_out.cpu()[live], plain_fp32(qkv[live][:, :hq], pos[live], table.cpu(), interleaved).to(q.dtype))
 
 
+def boundary_values(scale, g):
+    """32768 fp32 numbers: next to every rounding boundary of E4M3 times the scale, small, large, zero, not finite."""
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    ties = torch.cat([codes, (codes[1:] + codes[:-1]) / 2, torch.tensor([464.0, 512.0, 2.0 ** -12])])
+    near = (ties * float(scale)).float()
+    near = torch.cat([near] + [(near.view(torch.int32) + k).clamp(min=0).view(torch.float32) for k in (-3, -2, -1, 1, 2, 3)])
+    wide = torch.exp2(torch.rand(8000, generator=g) * 250 - 125)
+    x = torch.cat([near, wide, torch.tensor([0.0, float("inf"), 1e-45, 3e38])])
+    rest = torch.rand(16384 - x.numel(), generator=g) * 500 * float(scale)
+    x = torch.cat([x, rest])
+    return torch.cat([x, -x])
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_fp8_codes_are_those_of_the_fp32_quotient(pa, ty, interleaved):
+    """Bit by bit, at every rounding boundary and for every 16-bit value: K elements are made arbitrary fp32 numbers
+    by pairs (1, 0) and cosines of any size."""
+    T, d = 512, 128
+    g = torch.Generator().manual_seed(3)
+    step = 2.0 ** -23
+    scales = [1.0, 0.0125, 1 + step, 1 + 3 * step, 2 - step, 1.5 + step, 2.0 ** -60, 2.0 ** -61, 2.0 ** 60, 2.0 ** 61,
+              1e-30, 1e30, 1e-45, 1e-38, 3e38] + (torch.rand(12, generator=g) + 0.5).tolist()
+    x = torch.zeros((T, 3, d), dtype=ref.TYPES[ty])
+    x[:, 1, 0::2 if interleaved else 1] = 1.0
+    if not interleaved:
+        x[:, 1, 64:] = 0.0
+    x[:, 2] = torch.arange(65536).view(T, d).to(torch.uint16).view(x.dtype)
+    dev = x.cuda()
+    at = torch.arange(T, device="cuda")
+    for scale in scales:
+        scale = torch.tensor(scale, dtype=torch.float32)
+        table = torch.zeros((T, d))
+        table[:, :64] = boundary_values(scale, g).view(T, 64)
+        kc = torch.zeros((T // 16, 16, 1, d), dtype=torch.uint8, device="cuda")
+        vc, vc2 = torch.zeros_like(kc), torch.zeros_like(kc)
+        pa.rope_and_cache_fp8(dev[:, :1], dev[:, 1:2], dev[:, 2:], at, table.cuda(), kc, vc, at, float(scale), float(scale),
+                              interleaved=interleaved)
+        got = kc.cpu().view(T, d)
+        got = got[:, 0::2] if interleaved else got[:, :64]
+        want = (table[:, :64] / scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        nan = table[:, :64].isnan()       # (the neighbours of an infinity; a NaN's sign is not a value)
+        assert torch.equal(got[~nan], want[~nan]) and ((got[nan] & 0x7f) == 0x7f).all(), float(scale)
+        pa.reshape_and_cache_fp8(dev[:, 1:2].contiguous(), dev[:, 2:].contiguous(), torch.zeros_like(kc), vc2, at,
+                                 float(scale), float(scale))
+        assert torch.equal(vc, vc2), float(scale)
+
+
 def test_table(pa):
     for n, r, base in ((1, 2, 10000.0), (1000, 128, 10000.0), (131072, 64, 500000.0)):
         table = pa.rope_table(n, r, base).cpu().double()
