@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsParams p)
 // block_score_kernel gives every block an fp32 score with a bound on its error, and
 // block_select_kernel computes fp64 scores only for the blocks that the bound leaves in
 // doubt.  fp64 scores of all blocks cost 80 us for 8 x 8 x 2048 blocks and 8 heads (two
-// conversions to fp64 for each product, 16 a cycle and SM), the fp32 ones 16 (67 MB at
-// 4.2 TB/s, 64% of the copy bandwidth: each warp's chain of length, block id and rows).
+// conversions to fp64 for each product, 16 a cycle and SM), the fp32 ones 13 (67 MB at
+// 5 TB/s, 77% of the copy bandwidth: each warp's chain of length, block id and rows).
 struct SelectParams {
   const void *q;                  // [S][Hq][D]
   const uint4 *bounds;            // [NB][2][Hkv][16 chunks]
@@ -162,11 +162,9 @@ __device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, 
   }
   const size_t hi_off = static_cast<size_t>(p.num_kv_heads) * kChunksPerRow;
   uint4 lo[2][4], hi[2][4];
-  bool bad[2];   // no such block: left to the fp64 score, which puts it last
 #pragma unroll
   for (int r = 0; r < 2; ++r) {   // rows gid, gid + 8
     const int rid = __shfl_sync(kFullMask, id, gid + 8 * r);
-    bad[r] = rid < 0;
     const uint4 *src = p.bounds + (static_cast<size_t>(rid < 0 ? 0 : rid) * 2 * p.num_kv_heads + g) * kChunksPerRow + tig;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -199,7 +197,8 @@ __device__ __forceinline__ void score_tile(const SelectParams &p, int b, int g, 
 #pragma unroll
   for (int r = 0; r < 2; ++r) {   // s[2r], s[2r + 1]: row gid + 8 r, heads 2 tig, 2 tig + 1
     float best = -INFINITY, most = 0.f;
-    bool odd = bad[r];   // or not finite
+    // no such block, or not finite: left to the fp64 score (the former's puts it last)
+    bool odd = __shfl_sync(kFullMask, id, gid + 8 * r) < 0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * tig + e >= G) continue;
@@ -263,8 +262,11 @@ __device__ __forceinline__ void score_tile_f32(const SelectParams &p, int b, int
   }
 }
 
+// Six CTAs an SM: with the 80 registers a thread's 256 bytes are in flight at once (8 x 8 x
+// 2048 blocks, a pass of choice and decode: 43.3 us; eight CTAs 45.6, seven 44.7, five 45.7;
+// 64 x 8 x 2048, scores and choice: 119, 139, 131, 121).
 template <typename T, int G>
-__global__ void __launch_bounds__(kScoreWarps * 32, 8) block_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 6) block_score_kernel(const SelectParams p) {
   pdl_wait();
   pdl_trigger();
   int item = blockIdx.x;   // the heads of the same blocks side by side: their rows are neighbours in memory
@@ -285,8 +287,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 8) block_score_kernel(const 
 }
 
 // ---------------------------------------------------------------- choice
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectCached = 4096;     // fp32 scores kept in shared memory (more are read again from L2)
 constexpr int kSelectDoubt = 1024;      // blocks in doubt that the fast path takes
@@ -333,6 +333,7 @@ __device__ __noinline__ unsigned long long exact_key(const SelectParams &p, int 
 }
 
 // Exclusive sum of `x` over the CTA's threads, and the total.
+template <int NT>
 __device__ __forceinline__ int block_sum(int x, int *warp_s, int &total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int upto = x;
@@ -347,7 +348,7 @@ __device__ __forceinline__ int block_sum(int x, int *warp_s, int &total) {
   int before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) {
+  for (int w = 0; w < (NT / 32); ++w) {
     before += w < warp ? warp_s[w] : 0;
     total += warp_s[w];
   }
@@ -355,25 +356,26 @@ __device__ __forceinline__ int block_sum(int x, int *warp_s, int &total) {
 }
 
 // Element-wise largest of `x` over the CTA's threads.
+template <int NT>
 __device__ __forceinline__ float4 block_max(float4 x, float4 *warp_f) {
   x = make_float4(warp_max(x.x), warp_max(x.y), warp_max(x.z), warp_max(x.w));
   __syncthreads();   // warp_f of the previous call has been read
   if ((threadIdx.x & 31) == 0) warp_f[threadIdx.x >> 5] = x;
   __syncthreads();
-  const float4 y = warp_f[threadIdx.x & (kSelectWarps - 1)];
+  const float4 y = warp_f[threadIdx.x & ((NT / 32) - 1)];
   return make_float4(warp_max(y.x), warp_max(y.y), warp_max(y.z), warp_max(y.w));
 }
 
 // The `need` largest fp64 scores of blocks j0 .. j1-1, ties to the lowest index, for lists
 // that the fast path does not take: fp64 scores of all of them, then a radix select
 // that narrows the smallest chosen key 8 bits at a time, then the list itself.
-template <typename T, int G>
+template <typename T, int G, int NT>
 __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int g, int n, int j0, int j1, int need,
                                               unsigned long long *keys, int32_t *out, int *hist, int *warp_s,
                                               int *found) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int j = j0 + warp; j < j1; j += kSelectWarps) {
+  for (int j = j0 + warp; j < j1; j += (NT / 32)) {
     const unsigned long long key = exact_key<T, G>(p, b, g, j);
     if (lane == 0) keys[j] = key;
   }
@@ -382,10 +384,10 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
   int shift = 64;
   while (shift > 0) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 256; i += kSelectThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+    for (int j = j0 + threadIdx.x; j < j1; j += NT) {
       const unsigned long long key = keys[j];
       if (shift == 64 || (key >> shift) == prefix) atomicAdd(&hist[(key >> (shift - 8)) & 255], 1);
     }
@@ -404,7 +406,7 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
   }
   int written = 0, equal_before = 0;
 #pragma unroll 1
-  for (int base = 0; base < n; base += kSelectThreads) {
+  for (int base = 0; base < n; base += NT) {
     const int j = base + threadIdx.x;
     bool take = j < n && (j < j0 || j >= j1), equal = false;
     if (j >= j0 && j < j1) {
@@ -412,10 +414,10 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
       equal = keys[j] == prefix;
     }
     int total;
-    const int rank = block_sum(equal ? 1 : 0, warp_s, total);
+    const int rank = block_sum<NT>(equal ? 1 : 0, warp_s, total);
     if (equal && equal_before + rank < need) take = true;
     equal_before += total;
-    const int at = block_sum(take ? 1 : 0, warp_s, total);
+    const int at = block_sum<NT>(take ? 1 : 0, warp_s, total);
     if (take) out[written + at] = j;
     written += total;
   }
@@ -428,12 +430,13 @@ __device__ __noinline__ void select_all_exact(const SelectParams &p, int b, int 
 // [t0 - E, t1 + E]: an fp32 score above t1 + 2 E is chosen, one below t0 - 2 E is not,
 // and only the rest is in doubt and ranked by fp64 scores (one to three blocks for N(0, 1)
 // data; if more than kSelectDoubt, or more blocks than kSelectMaxBlocks, select_all_exact
-// decides).  9 us for 8 CTAs of 2048 blocks, 10 for 64: its length is a dozen
-// block-wide steps of 500 to 2000 cycles whose code runs once.  Bisection in
-// registers in the histogram's place was as long (13300 cycles against 14400) and slower
-// for 488 CTAs; 256 threads are slower for few CTAs (19.8 against 18.5 a pass).
-template <typename T, int G>
-__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const SelectParams p) {
+// decides).  Its length, 8 us for 8 lists of 2048 blocks, is that of a dozen CTA-wide steps
+// of 200 to 1300 cycles.  A thread keeps its first NT / 128 scores in registers (17.2 us a pass
+// of choice and decode for one sequence; 18.5 with every score in shared memory).  Slower:
+// bisection in the histogram's place; a first run through the code on a made-up
+// list while the scores are computed, to have it in the instruction cache (19.7).
+template <typename T, int G, int NT>
+__global__ void __launch_bounds__(NT) block_select_kernel(const SelectParams p) {
   __shared__ union {
     int hist[kSelectBins];
     unsigned bits[kSelectMaxBlocks / 32];   // chosen blocks
@@ -441,8 +444,8 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   __shared__ float score_s[kSelectCached];
   __shared__ unsigned long long doubt_key[kSelectDoubt];
   __shared__ int doubt_j[kSelectDoubt];
-  __shared__ int warp_s[kSelectWarps];
-  __shared__ float4 warp_f[kSelectWarps];
+  __shared__ int warp_s[NT / 32];
+  __shared__ float4 warp_f[NT / 32];
   __shared__ int found[2];
   __shared__ int num_doubt, num_in;
   static_assert(kSelectMaxBlocks / 32 <= kSelectBins, "the bits take the histogram's place");
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   if (n <= K) {
     if (bad && threadIdx.x == 0) record_error(4 /*PA_DEV_BAD_CONTEXT_LEN*/, b);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < n ? i : -1;
+    for (int i = threadIdx.x; i < K; i += NT) out[i] = i < n ? i : -1;
     return;
   }
   const float2 *approx = p.approx + static_cast<size_t>(blockIdx.x) * p.max_blocks;
@@ -467,8 +470,28 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- range and error of the fp32 scores; NaN marks the blocks that are in doubt anyway
   float top = -INFINITY, low = INFINITY, err = 0.f, odd = 0.f;
-#pragma unroll 4
-  for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+  constexpr int kReg = NT / 128;
+  float2 ar[kReg];
+#pragma unroll
+  for (int k = 0; k < kReg; ++k) {
+    const int j = j0 + threadIdx.x + k * NT;
+    ar[k] = j < j1 ? approx[j] : make_float2(0.f, INFINITY);
+  }
+  float xr[kReg];
+#pragma unroll
+  for (int k = 0; k < kReg; ++k) {
+    const bool fine = ar[k].y < INFINITY;
+    xr[k] = fine ? ar[k].x : __int_as_float(0x7fffffff);
+    if (fine) {
+      top = fmaxf(top, ar[k].x);
+      low = fminf(low, ar[k].x);
+      err = fmaxf(err, ar[k].y);
+    } else if (j0 + threadIdx.x + k * NT < j1) {
+      odd = 1.f;
+    }
+  }
+#pragma unroll 1
+  for (int j = j0 + threadIdx.x + kReg * NT; j < j1; j += NT) {
     const float2 x = approx[j];
     const bool fine = x.y < INFINITY;
     if (j < kSelectCached) score_s[j] = fine ? x.x : __int_as_float(0x7fffffff);
@@ -481,12 +504,12 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     }
   }
 #pragma unroll 1
-  for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) u.hist[i] = 0;
+  for (int i = threadIdx.x; i < kSelectBins; i += NT) u.hist[i] = 0;
   if (threadIdx.x == 0) {
     num_doubt = num_in = 0;
     found[0] = -1;
   }
-  const float4 range = block_max(make_float4(top, -low, err, odd), warp_f);
+  const float4 range = block_max<NT>(make_float4(top, -low, err, odd), warp_f);
   top = range.x;
   low = -range.y;
   err = 2.f * range.z;
@@ -501,19 +524,25 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   auto bin = [&](float x) { return min(kSelectBins - 1, static_cast<int>((x - low) * scale)); };   // grows with x
   float t0 = -INFINITY, t1 = INFINITY;   // no block with a finite score: all are in doubt
   if (need > 0) {
+    int br[kReg];
+#pragma unroll
+    for (int k = 0; k < kReg; ++k) {
+      br[k] = xr[k] == xr[k] ? bin(xr[k]) : -1;
+      if (br[k] >= 0) atomicAdd(&u.hist[br[k]], 1);
+    }
 #pragma unroll 1
-    for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+    for (int j = j0 + threadIdx.x + kReg * NT; j < j1; j += NT) {
       const float x = score(j);
       if (x == x) atomicAdd(&u.hist[bin(x)], 1);
     }
     __syncthreads();
     // the bin of the need-th largest (thread t: bins from the top down, 4 t .. 4 t + 3)
-    constexpr int kPer = kSelectBins / kSelectThreads;
+    constexpr int kPer = kSelectBins / NT;
     int mine = 0;
 #pragma unroll
     for (int d = 0; d < kPer; ++d) mine += u.hist[kSelectBins - 1 - kPer * threadIdx.x - d];
     int total;
-    int above = block_sum(mine, warp_s, total);
+    int above = block_sum<NT>(mine, warp_s, total);
     if (above < need && above + mine >= need) {
       int d = kSelectBins - 1 - kPer * threadIdx.x;
       while (above + u.hist[d] < need) above += u.hist[d--];
@@ -523,15 +552,21 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     const int at = found[0];
     float a = INFINITY, z = -INFINITY;
     if (at >= 0) {
+#pragma unroll
+      for (int k = 0; k < kReg; ++k)
+        if (br[k] == at) {
+          a = fminf(a, xr[k]);
+          z = fmaxf(z, xr[k]);
+        }
 #pragma unroll 1
-      for (int j = j0 + threadIdx.x; j < j1; j += kSelectThreads) {
+      for (int j = j0 + threadIdx.x + kReg * NT; j < j1; j += NT) {
         const float x = score(j);
         if (x == x && bin(x) == at) {
           a = fminf(a, x);
           z = fmaxf(z, x);
         }
       }
-      const float4 edge = block_max(make_float4(-a, z, 0.f, 0.f), warp_f);
+      const float4 edge = block_max<NT>(make_float4(-a, z, 0.f, 0.f), warp_f);
       t0 = -edge.x - err;
       t1 = edge.y + err;
     }
@@ -540,11 +575,27 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   // ---- chosen, not chosen, in doubt.  (Blocks without a finite fp32 score may be above any other
   // and take its place: with some, nothing is certain to be chosen; what is below t0 is still out.)
 #pragma unroll 1
-  for (int i = threadIdx.x; i < kSelectMaxBlocks / 32 && i * 32 < n; i += kSelectThreads) u.bits[i] = 0u;
+  for (int i = threadIdx.x; i < kSelectMaxBlocks / 32 && i * 32 < n; i += NT) u.bits[i] = 0u;
   __syncthreads();
   const bool fast = n <= kSelectMaxBlocks;
+#pragma unroll
+  for (int k = 0; k < kReg; ++k) {
+    const int j = j0 + threadIdx.x + k * NT;
+    const float x = xr[k];
+    const bool live = j < j1 && need > 0 && fast;
+    const bool in = live && !any_odd && x > t1;
+    const bool doubt = live && !in && !(x < t0);
+    if (in) {
+      atomicAdd(&num_in, 1);
+      atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+    }
+    if (doubt) {
+      const int at = atomicAdd(&num_doubt, 1);
+      if (at < kSelectDoubt) doubt_j[at] = j;
+    }
+  }
 #pragma unroll 1
-  for (int base = j0; base < j1 && need > 0 && fast; base += kSelectThreads) {
+  for (int base = j0 + kReg * NT; base < j1 && need > 0 && fast; base += NT) {
     const int j = base + threadIdx.x;
     const float x = j < j1 ? score(j) : -INFINITY;
     const bool in = j < j1 && !any_odd && x > t1;
@@ -563,25 +614,25 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
   const int left = need - num_in;   // how many of the blocks in doubt are chosen
   if (need > 0 && (!fast || m > kSelectDoubt || left < 0)) {
     __syncthreads();
-    select_all_exact<T, G>(p, b, g, n, j0, j1, need, p.keys + static_cast<size_t>(blockIdx.x) * p.max_blocks, out,
+    select_all_exact<T, G, NT>(p, b, g, n, j0, j1, need, p.keys + static_cast<size_t>(blockIdx.x) * p.max_blocks, out,
                            u.hist, warp_s, found);
     return;
   }
   if (!fast) {   // need == 0: the first and last blocks alone
 #pragma unroll 1
-    for (int i = threadIdx.x; i < K; i += kSelectThreads) out[i] = i < j0 ? i : n - K + i;
+    for (int i = threadIdx.x; i < K; i += NT) out[i] = i < j0 ? i : n - K + i;
     return;
   }
   if (m > left) {
 #pragma unroll 1
-    for (int i = warp; i < m; i += kSelectWarps) {
+    for (int i = warp; i < m; i += (NT / 32)) {
       const unsigned long long key = exact_key<T, G>(p, b, g, doubt_j[i]);
       if (lane == 0) doubt_key[i] = key;
     }
     __syncthreads();
   }
 #pragma unroll 1
-  for (int i = threadIdx.x; i < m; i += kSelectThreads) {
+  for (int i = threadIdx.x; i < m; i += NT) {
     const int j = doubt_j[i];
     int before = 0;   // blocks in doubt that are chosen before this one
     if (m > left) {
@@ -592,18 +643,18 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(const Sele
     if (before < left) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
   }
 #pragma unroll 1
-  for (int j = threadIdx.x; j < j0; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+  for (int j = threadIdx.x; j < j0; j += NT) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
 #pragma unroll 1
-  for (int j = j1 + threadIdx.x; j < n; j += kSelectThreads) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
+  for (int j = j1 + threadIdx.x; j < n; j += NT) atomicOr(&u.bits[j >> 5], 1u << (j & 31));
   __syncthreads();
   // ---- the list
   int written = 0;
   const int words = (n + 31) / 32;
 #pragma unroll 1
-  for (int base = 0; base < words; base += kSelectThreads) {
+  for (int base = 0; base < words; base += NT) {
     unsigned w = base + threadIdx.x < words ? u.bits[base + threadIdx.x] : 0u;
     int total;
-    int at = written + block_sum(__popc(w), warp_s, total);
+    int at = written + block_sum<NT>(__popc(w), warp_s, total);
     for (; w != 0u; w &= w - 1u) out[at++] = (base + threadIdx.x) * 32 + __ffs(w) - 1;
     written += total;
   }
