@@ -363,8 +363,10 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
  * workspace     pa_decode_shared_prefix_workspace_bytes(...) bytes, 256-byte
  *               aligned; scratch.  Calls that overlap on the GPU need one each.
  * dtype PA_F16 or PA_BF16, head_dim 128, group size (num_heads / num_kv_heads) 1,
- * 2, 4 or 8.  Accumulation is fp32; softmax weights enter the prefix's P V as
- * fp16 (relative rounding 2^-11, PA_F16) or as two bf16 parts (2^-15, PA_BF16).
+ * 2, 4 or 8.  Accumulation is fp32; softmax weights enter the prefix's P V in two
+ * parts of the cache's type, off by less than 2^-20 of the weight or 2^-31 of the
+ * row's largest weight in the same partition of the prefix, whichever is more
+ * (PA_F16), or by less than 2^-15 of the weight (PA_BF16).
  * Bad block ids of a prefix read as zeros (PA_DEV_BAD_BLOCK_ID).
  * Errors: as pa_decode, PA_ERR_DTYPE for other types, PA_ERR_SHAPE also for
  * num_seqs > 0 without groups, a max_prefix_len off 16 and more than 2^31 - 1 CTAs.

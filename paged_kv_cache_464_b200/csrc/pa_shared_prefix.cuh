@@ -23,10 +23,11 @@
 // Warps (384 threads):
 //   0-3, 4-7  softmax: tcgen05.ld of the row's 128 scores, maximum, O rescaled only
 //             when a row's maximum grows by more than 2^8, exponentials, P written
-//             over S, 32 scores' place at a time (fp16 caches: one fp16 part, relative
-//             rounding 2^-11; bf16 caches: the upper 16 bits and what they leave, 2^-15
-//             together, so that V needs no conversion and has no range limit: twice
-//             the P V products, 5 us of 52 below), handed over in two halves of 64 tokens;
+//             over S, 32 scores' place at a time, as two parts in the cache's type (the
+//             weight cut to its upper bits, and what they leave, rounded), so that V needs
+//             no conversion and has no range limit and no weight is rounded to 16 bits:
+//             twice the P V products, 5 us of 52 below; handed over in two halves of 64
+//             tokens;
 //   8, 9      tensor-core issue for w = 0, 1 (one thread each);
 //   10, 11    TMA: pair: warp 10 fills one ring of 5 stages for both; split: warp 10 + w
 //             fills w's own ring of 3.  Items alternate K(i), V(i): S has one
@@ -150,34 +151,53 @@ __device__ __forceinline__ float row_max(const float *s) {
   return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
 }
 
-// P = 2^((s - m) c2) of the 32 scores in columns taddr .. taddr + 31, written over them: 16
-// columns of pairs (the upper 16 bits as they are for bf16, rounded for fp16)
-// and, for bf16, 16 columns of what those leave, rounded.  Scores from `live` on
+// Weights enter P V as hi + lo.  bf16: hi has the upper 8 of 24 bits, lo the next 8: off by
+// less than 2^-15 of the weight.  fp16: 11 and 11 bits, 2^-20, as long as neither is
+// subnormal (spaced 2^-24), and the largest row weights are 1 (up to 2^8 before a rescale).
+// So fp16 weights are 2^7 times larger (2^15 at most, of 65504): what is lost of a small
+// one is below 2^-24 of those units, 2^-31 of the row's largest weight.  The partial's
+// maximum is stored 7 lower, which takes the factor out again.
+template <typename T>
+struct PrefixWeights;
+template <>
+struct PrefixWeights<__nv_bfloat16> {
+  static constexpr float kBias = 0.f;
+  static constexpr uint32_t kUpper = 0xffff0000u;   // the bits of fp32 that hi holds
+  __device__ __forceinline__ static uint32_t pack_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+};
+template <>
+struct PrefixWeights<__half> {
+  static constexpr float kBias = 7.f;
+  static constexpr uint32_t kUpper = 0xffffe000u;
+  __device__ __forceinline__ static uint32_t pack_hi(uint32_t a, uint32_t b) {   // exact but for subnormals
+    return Pack16<__half>::pack(__uint_as_float(a & kUpper), __uint_as_float(b & kUpper));
+  }
+};
+
+// P = 2^(s c2 + nmc) of the 32 scores in columns taddr .. taddr + 31, written over them: 16
+// columns of pairs of upper parts, then 16 of lower ones.  Scores from `live` on
 // count for nothing.  Adds the sums of even and odd columns to `sum`.
-template <typename PK, bool kLo>
+template <typename T>
 __device__ __forceinline__ void exp_chunk(uint32_t taddr, int live, float2 cc2, float2 nmc, float2 &sum) {
+  using W = PrefixWeights<T>;
   float s[32];
   tmem_ld32(taddr, s);
   if (live < 32) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) s[k] = k < live ? s[k] : -INFINITY;
   }
-  uint32_t hi[16], lo[kLo ? 16 : 1];
+  uint32_t hi[16], lo[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const float2 x = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), cc2, nmc);
     const float2 e = make_float2(ex2(x.x), ex2(x.y));
     sum = __fadd2_rn(sum, e);
-    if constexpr (kLo) {
-      const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
-      hi[k] = __byte_perm(ux, uy, 0x7632);
-      lo[k] = PK::pack(e.x - __uint_as_float(ux & 0xffff0000u), e.y - __uint_as_float(uy & 0xffff0000u));
-    } else {
-      hi[k] = PK::pack(e.x, e.y);
-    }
+    const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
+    hi[k] = W::pack_hi(ux, uy);
+    lo[k] = Pack16<T>::pack(e.x - __uint_as_float(ux & W::kUpper), e.y - __uint_as_float(uy & W::kUpper));
   }
   tmem_st16u(taddr, hi);
-  if constexpr (kLo) tmem_st16u(taddr + 16, lo);
+  tmem_st16u(taddr + 16, lo);
 }
 
 template <typename T, int G>
@@ -187,7 +207,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   using SM = PrefixSmem;
   using PK = Pack16<T>;
   constexpr int D = 128;
-  constexpr bool kLo = PK::kFormat == 1;   // bf16: P in two parts
+  constexpr float kBias = PrefixWeights<T>::kBias;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -404,7 +424,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {   // 16 tokens = 8 columns of P a step
             const uint32_t p_tmem = s_tmem + 32 * (kk >> 1) + 8 * (kk & 1);   // 16 columns of P, 16 of its low parts
             umma_f16_ts(o_tmem, p_tmem, v0 + ((kk * 16 * 128) >> 4), kIdescPV, i > 0 || kk > 0);
-            if constexpr (kLo) umma_f16_ts(o_tmem, p_tmem + 16, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
+            umma_f16_ts(o_tmem, p_tmem + 16, v0 + ((kk * 16 * 128) >> 4), kIdescPV, true);
           }
         }
         if (!ok) break;
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint64_t *tb = tile_bars + 4 * w;
     const float c2 = p.scale_log2;
     float m_run = -INFINITY;   // reference maximum of this row's raw scores
-    float l_run = 0.f;         // sum of 2^((s - m_run) c2)
+    float l_run = 0.f;         // sum of the weights, 2^((s - m_run) c2 + kBias)
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (!ok) return;
@@ -480,16 +500,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       // The scores are read a second time, 32 a turn of a short loop: with all 128 in line the
       // kernel was 68 KB of instructions, which its roles (and the neighbouring SM's) evict
       // from the cache between them: 83.7 us a call against 75.2 (64 sequences x 32768 tokens).
-      const float2 nmc = make_float2(-m_run * c2, -m_run * c2), cc2 = make_float2(c2, c2);
+      const float nm = fmaf(-m_run, c2, kBias);
+      const float2 nmc = make_float2(nm, nm), cc2 = make_float2(c2, c2);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
-        exp_chunk<PK, kLo>(t_s + 32 * c, live - 32 * c, cc2, nmc, sum);
+        exp_chunk<T>(t_s + 32 * c, live - 32 * c, cc2, nmc, sum);
         if (c & 1) hand_over(&tb[1 + (c >> 1)]);
       }
       l_run += sum.x + sum.y;
     }
-    // ---- this warp's 32 rows of partials: m in base-2 units, o and l relative to it.  In
+    // ---- this warp's 32 rows of partials: m in base-2 units (less kBias), o and l relative to it.  In
     // the workspace they are consecutive, so o goes through shared memory (Q and the
     // K/V stages, free once both warpgroups' products are complete; 16-byte chunk c
     // of row r at c ^ (r & 31)) and out 512 consecutive bytes a warp store.  A thread
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const int rw = row0 + (split ? 0 : w * kPrefixRows) + (r & ~31);   // the warp's first row
     const size_t at = prefix_slot(p, g, split ? 2 * part + w : part) + static_cast<size_t>(s0) * G + rw;
     if (ok && rw + lane < rows_group) {
-      p.ws_m[at + lane] = n > 0 ? m_run * c2 : -INFINITY;
+      p.ws_m[at + lane] = n > 0 ? -fmaf(-m_run, c2, kBias) : -INFINITY;
       p.ws_l[at + lane] = l_run;
     }
     if (softmax_all(ok) && n > 0) {

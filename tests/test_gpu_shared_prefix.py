@@ -1,6 +1,8 @@
 """Shared-prefix decode against the plain 64-bit attention, over group sizes
 around the 128-row tiles, prefixes around the 128-token tiles, ragged and empty
 suffixes, and its error paths."""
+import math
+
 import pytest
 import torch
 
@@ -217,3 +219,48 @@ def test_blocks_past_four_gigabytes(pa):
     out = pa.decode_shared_prefix(q.cuda(), k, v, far.cuda(), lens.cuda(), gs.cuda(), pl.cuda(), 0.088).cpu()
     want, weight = ref.attention(q, ks, vs, tables, lens, 0.088)
     assert ((out.double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 16)).all()
+
+
+@pytest.mark.parametrize("size", [3, 60])
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("level", [12.0, 19.6, 24.4, 25.7])
+def test_tail_under_a_dominant_key(pa, ty, level, size):
+    """One key that outweighs every other by 2^level and has no value: the output is the rest of the prefix alone."""
+    q, k, v, tables, _, lens, gs, pl = make([size], [8192], lambda b: 0, 1, 4, ty, seed=11)
+    ids = tables[0, :512].long()
+    k[ids] = 0.0
+    k[ids[100], 5, 0, 0] = level * math.log(2.0) / (0.088 * 8)
+    q[:], q[..., 0] = 0.0, 8.0
+    v[ids] = v[ids].abs() + 0.5
+    v[ids[100], 5] = 0.0
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    args = [t.cuda() for t in (q, k, v, tables, lens, gs, pl)]
+    err = (pa.decode_shared_prefix(*args, 0.088).cpu().double() - want).abs()
+    # the largest score, 25.7 ln 2 = 17.9 at scale, is a single product: attention_tolerance's 2^-13 covers it; each of
+    # the 8192 weights is off by 2^-31 of the largest beside its relative error (fp16), |V| is at most weight's own mean
+    # of it times 8 (0.5 + |N(0, 1)|, mean 1.3, largest of a million 5.4); half a step of a subnormal fp16 output is 2^-25
+    tol = ref.attention_tolerance(want, weight, ty, P_BITS[ty]) - 1e-7 + 8192 * 2.0 ** -31 * 8 * 1.3 * 2.0 ** -13 + 2.0 ** -25
+    assert (err <= tol).all(), ((err - tol).max(), err.max(), want.abs().max())
+
+
+@pytest.mark.parametrize("ty,bits", [("f16", 20), ("bf16", 15)])
+@pytest.mark.parametrize("size", [3, 60])
+def test_weights_of_two_kinds_that_nearly_cancel(pa, ty, bits, size):
+    """Half of the tokens of weight 1 and value 1, half of weight 0.5 + 2^-12 (halfway between two fp16 numbers) and
+    value -2: what is left is 1/2000 of either half."""
+    q, k, v, tables, _, lens, gs, pl = make([size], [2048], lambda b: 0, 1, 4, ty, seed=12)
+    ids = tables[0, :128].long()
+    score = math.log(0.5 + 2.0 ** -12) / 0.088
+    first = torch.tensor(score / 8).to(k.dtype)
+    q[:] = 0.0
+    q[..., 0], q[..., 1] = 8.0, 2.0 ** -6
+    k[ids], v[ids] = 0.0, 1.0
+    k[ids, 1::2, 0, 0], k[ids, 1::2, 0, 1] = first, ((score - 8 * first.double()) * 2 ** 6).to(k.dtype)
+    v[ids, 1::2] = -2.0
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    assert (want.abs() < 2.0 ** -10 * weight).all() and (want.abs() > 2.0 ** -13 * weight).all()
+    out = pa.decode_shared_prefix(*[t.cuda() for t in (q, k, v, tables, lens, gs, pl)], 0.088).cpu()
+    # the weights' relative error; a score of two products below 8 (2^-24 each) times scale, the exponential (2^-22),
+    # and sums of 2048 products over 16 steps of 128 tokens each: below 2^-18 together
+    tol = ref.HALF_STEP[ty] * want.abs() + (2.0 ** -bits + 2.0 ** -18) * weight + 2.0 ** -25
+    assert ((out.double() - want).abs() <= tol).all(), ((out.double() - want).abs() / weight).max()
