@@ -6,6 +6,7 @@ has not been built -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -110,6 +111,17 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream: Optional[torch.cuda.Stream]):
+    """The stream that a call runs on, as the current one: for reading a length that may have been written on it a
+    moment ago, and for allocating what only the call uses."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _largest(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
+    with _on(stream):
+        return int(t.max().item()) if t.numel() else 0
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -177,7 +189,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -212,7 +224,7 @@ def decode_append(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cac
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -297,7 +309,7 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -329,7 +341,8 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block
     if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start_loc.numel() != S + 1:
         raise ValueError("block_tables must be [S, MBS] and query_start_loc [S + 1]")
     if max_query_len is None:
-        qsl = query_start_loc.cpu()
+        with _on(stream):
+            qsl = query_start_loc.cpu()
         max_query_len = int((qsl[1:] - qsl[:-1]).max()) if S else 0
     if out is None:
         out = torch.empty_like(q)
@@ -537,14 +550,16 @@ def decode_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         _refuse("q k_cache v_cache block_tables context_lens group_start prefix_lens",
                 (q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens), 7)
     if max_prefix_len is None or max_suffix_len is None or max_group_size is None:
-        starts, prefixes = group_start.cpu().long(), prefix_lens.cpu().long()
+        with _on(stream):
+            starts, prefixes = group_start.cpu().long(), prefix_lens.cpu().long()
         sizes = (starts[1:] - starts[:-1]).clamp(min=0)
         if max_group_size is None:
             max_group_size = int(sizes.max()) if n else 0
         if max_prefix_len is None:
             max_prefix_len = int(prefixes.max()) if n else 0
         if max_suffix_len is None:
-            own = context_lens.cpu().long()
+            with _on(stream):
+                own = context_lens.cpu().long()
             if int(sizes.sum()) == S:
                 own = own - prefixes.repeat_interleave(sizes)
             max_suffix_len = max(0, int(own.max())) if S else 0
@@ -584,7 +599,7 @@ def update_block_bounds(k_cache: torch.Tensor, block_bounds: torch.Tensor, block
         _refuse("k_cache block_bounds block_tables context_lens new_lens",
                 (k_cache, block_bounds, block_tables, context_lens, new_lens), 5)
     if max_new_len is None:
-        max_new_len = int(new_lens.max()) if S else 0
+        max_new_len = _largest(new_lens, stream)
     _launch(_lib.pa_update_block_bounds, "pa_update_block_bounds", index, stream, k_cache.data_ptr(),
             block_bounds.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
             new_lens.data_ptr(), S, max_new_len, nb, bs, hkv, d, dt)
@@ -615,7 +630,7 @@ def select_blocks(q: torch.Tensor, block_bounds: torch.Tensor, block_tables: tor
             selected.get_device() != index or not selected.is_contiguous():
         raise ValueError("selected must be a contiguous int32 [S, num_kv_heads, K]")
     if max_context_len is None:
-        max_context_len = int(context_lens.max()) if S else 0
+        max_context_len = _largest(context_lens, stream)
     need = _lib.pa_select_blocks_workspace_bytes(S, hkv, max_context_len) if workspace is None else 0
     workspace, ws_ptr, ws_bytes = _workspace(need, workspace, index, stream)
     _launch(_lib.pa_select_blocks, "pa_select_blocks", index, stream, selected.data_ptr(), q.data_ptr(),
