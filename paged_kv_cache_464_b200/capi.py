@@ -173,8 +173,8 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     """Paged decode attention.  q [S, Hq, D]; block_tables [S, MBS] int32; context_lens [S] int32.
 
     ``max_context_len`` should be passed by callers that know it (reading it
-    from ``context_lens`` costs a device-to-host sync).  ``workspace`` is
-    allocated here when needed and not given.
+    from ``context_lens`` costs a device-to-host sync).  ``workspace`` and
+    ``out`` are allocated here, on ``stream``, when needed and not given.
     """
     nb, bs, hkv, d, dt = _cache_args(k_cache, v_cache)
     S, hq, dq = q.shape
@@ -185,14 +185,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq] and context_lens [S]")
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
         max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_lib.pa_decode(_dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
@@ -220,14 +222,16 @@ def decode_append(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor, k_cac
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq] and context_lens [S]")
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
         max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_lib.pa_decode_append(_dev(out, "out"), _dev(q, "q"), _dev(key, "key"), _dev(value, "value"),
@@ -260,7 +264,8 @@ def decode_static_workspace(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq] and context_lens [S]")
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     _check(_lib.pa_decode_static_workspace(
@@ -305,14 +310,16 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.numel() != S:
         raise ValueError("block_tables must be [S, max_blocks_per_seq] and context_lens [S]")
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     if max_context_len is None:
         max_context_len = _largest(context_lens, stream)
     need = decode_workspace_bytes(S, hq, hkv, d, max_context_len, partition_size)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_lib.pa_decode_fp8(_dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
@@ -345,7 +352,8 @@ def prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block
             qsl = query_start_loc.cpu()
         max_query_len = int((qsl[1:] - qsl[:-1]).max()) if S else 0
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must match q")
     _check(_lib.pa_prefill(_dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
@@ -394,7 +402,7 @@ def _launch(fn, where: str, index: int, stream: Optional[torch.cuda.Stream], *ar
 def _empty(shape, dtype: torch.dtype, index: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=index)
-    with torch.cuda.stream(stream):
+    with _on(stream):
         return torch.empty(shape, dtype=dtype, device=index)
 
 

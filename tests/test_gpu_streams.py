@@ -89,3 +89,26 @@ def test_maxima_are_those_of_the_calls_stream(pa, name):
     s.synchronize()
     assert pa.get_device_error(clear=True) == (0, 0)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_what_a_call_allocates_is_its_streams(pa, name, monkeypatch):
+    """(Scratch of another stream could be handed out again while the call still runs.)"""
+    b = Batch(pa, fp8=name == "decode_fp8")
+    b.finish()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    seen = []
+    for make in ("empty", "empty_like"):
+        real = getattr(torch, make)
+
+        def watched(*args, real=real, **kwargs):
+            t = real(*args, **kwargs)
+            if t.is_cuda:
+                seen.append(torch.cuda.current_stream())
+            return t
+        monkeypatch.setattr(pa.torch, make, watched)
+    CALLS[name](pa, b, s)
+    monkeypatch.undo()
+    s.synchronize()
+    assert all(x == s for x in seen) and (seen or name == "bounds")
