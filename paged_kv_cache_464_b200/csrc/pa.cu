@@ -4,6 +4,7 @@
 // unit so that the per-device error word needs no separate device linking.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -803,14 +804,18 @@ pa_status_t pa_rope_and_cache_fp8(void *q_out, const void *q, const void *key, c
 // ---------------------------------------------------------------- shared prefix
 namespace {
 
-// How pa_decode_shared_prefix cuts its work: partitions of the prefix, and the
-// suffix's split-K; the workspace has `slots` partials a row, the suffix's from slot0 on.
+// How pa_decode_shared_prefix cuts its work: partitions of the prefix (by the work that the
+// device finds, pa::prefix_part_tiles), and the suffix's split-K; the workspace has `slots`
+// partials a row, the suffix's from slot0 on.
 struct PrefixPlan {
-  int row_ctas, parts, part_tokens, suffix_partition, suffix_parts, slot0, slots;
+  int levels, most_row_ctas, part_tiles[pa::kPrefixLevels];
+  double ctas;   // of the prefix kernel
+  int suffix_partition, suffix_parts, slot0, slots;
   WorkspaceLayout ws;
 };
 
-// Partitions: as many as give the shortest run by this model, in us measured on B200.  A
+// Tiles of a partition, for `ctas` (256 rows, KV head) pairs over `tiles` tiles: as many
+// partitions as give the shortest run by this model, in us measured on B200.  A
 // CTA (one an SM) takes 8.5 of set-up and epilogue and 2.9 a step; a step is a
 // tile, or two where a CTA has at most 128 rows.  A last wave that is not full counts for
 // at least half.  Each partition's partials cost 0.35 to combine and their
@@ -818,36 +823,58 @@ struct PrefixPlan {
 // the two partitions chosen, 52.5 with one, 51.2 with three; 128 sequences over 1024 tokens:
 // 38.0 with four, 39.2 with three, 39.5 with eight; 5 over 4000: 15.9 with eight, 16.5 with
 // sixteen, 24.6 with three.)
+int plan_part_tiles(double ctas, int tiles, bool split, double partial_us) {
+  const double sms = sm_count();
+  double best = 1e300;
+  int per = tiles, last = 0;
+  for (int parts = 1; parts <= tiles && parts <= 64; ++parts) {
+    const int t = (tiles + parts - 1) / parts;
+    if (t == last) continue;
+    last = t;
+    const int steps = split ? (t + 1) / 2 : t;
+    const double waves = ctas * parts / sms, full = std::floor(waves), rest = waves - full;
+    const double runs = waves <= 1 ? 1 : full + (rest > 0 ? (rest > 0.5 ? rest : 0.5) : 0);
+    const double cost = runs * (8.5 + 2.9 * steps) + parts * partial_us;
+    if (cost < best) {
+      best = cost;
+      per = t;
+    }
+  }
+  return per;
+}
+
 PrefixPlan plan_prefix(int num_seqs, int num_groups, int num_heads, int num_kv_heads, int head_dim, int max_prefix_len,
                        int max_suffix_len, int max_group_size) {
   PrefixPlan r{};
   const int group = num_heads / num_kv_heads;
-  const int rows = max_group_size * group;
-  r.row_ctas = (rows + 2 * pa::kPrefixRows - 1) / (2 * pa::kPrefixRows);
+  const int rows = max_group_size * group, cta_rows = 2 * pa::kPrefixRows;
   const int tiles = (max_prefix_len + pa::kPrefixKv - 1) / pa::kPrefixKv;
+  int most_parts = 0;
   if (tiles > 0) {
-    const double ctas = (double)num_groups * r.row_ctas * num_kv_heads;
-    const double sms = sm_count();
+    // 256 rows at a time: no group has more than the largest, and all of them no more than the batch and a rest each
+    const double most = std::min((double)num_groups * ((rows + cta_rows - 1) / cta_rows),
+                                 num_groups + std::floor((double)num_seqs * group / cta_rows));
+    r.most_row_ctas = (int)std::min(most, (double)INT32_MAX);
     const double partial_us = 0.35 + (double)num_seqs * num_heads * 2 * head_dim * sizeof(float) / 6.5e6;
-    double best = 1e300;
-    int per = tiles;
-    for (int parts = 1; parts <= tiles && parts <= 64; ++parts) {
-      const int t = (tiles + parts - 1) / parts;
-      const int steps = rows <= pa::kPrefixRows ? (t + 1) / 2 : t;
-      const double waves = ctas * parts / sms, full = std::floor(waves), rest = waves - full;
-      const double runs = waves <= 1 ? 1 : full + (rest > 0 ? (rest > 0.5 ? rest : 0.5) : 0);
-      const double cost = runs * (8.5 + 2.9 * steps) + parts * partial_us;
-      if (cost < best) {
-        best = cost;
-        per = t;
-      }
+    // With one group its rows are the work; with more, the device says which of the levels it is
+    // (in 32 bits, so beyond them it is taken to be all that the bounds allow).
+    const int levels = num_groups == 1 || most * tiles >= 2147483648.0 ? 1 : pa::kPrefixLevels;
+    for (int i = 0; i < levels; ++i) {
+      const double live = (double)((r.most_row_ctas + (1ll << i) - 1) >> i);
+      const int per = plan_part_tiles(live * num_kv_heads, tiles, rows <= pa::kPrefixRows, partial_us);
+      const int parts = (tiles + per - 1) / per;
+      r.part_tiles[i] = per;
+      r.levels = i + 1;
+      most_parts = std::max(most_parts, parts);
+      // Each 256 rows' first partition may be as short as a tile; every further one takes a whole one before it.
+      const double first = std::min(most, live * tiles);
+      r.ctas = std::max(r.ctas, std::min(first + std::floor((live * tiles - first) / per), most * parts) * num_kv_heads);
+      if (live <= 1) break;
     }
-    r.part_tokens = per * pa::kPrefixKv;
-    r.parts = (tiles + per - 1) / per;
   }
   r.suffix_partition = resolve_partition_size(num_seqs, num_heads, num_kv_heads, head_dim, max_suffix_len, 0);
   r.suffix_parts = max_partitions(max_suffix_len, r.suffix_partition);
-  r.slot0 = 2 * r.parts;
+  r.slot0 = 2 * most_parts;
   r.slots = r.slot0 + r.suffix_parts;
   const size_t n = (size_t)num_seqs * num_heads * r.slots;
   r.ws.l_off = align256(n * sizeof(float));
@@ -869,15 +896,14 @@ pa_status_t prefix_shape_status(int num_seqs, int num_groups, int num_heads, int
 }
 
 template <typename T, int G, typename Math>
-pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa::PrefixParams &p, int num_groups,
+pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa::SuffixParams &p, unsigned prefix_ctas,
                           cudaStream_t stream) {
   pa_status_t st;
-  if (p.parts > 0) {
+  if (prefix_ctas > 0) {
     auto kernel = pa::pa_shared_prefix_kernel<T, G>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pa::PrefixSmem::kAlloc) != cudaSuccess)
       return PA_ERR_CUDA;
-    const unsigned grid = (unsigned)(num_groups * p.row_ctas * p.num_kv_heads * p.parts);
-    st = launch(kernel, dim3(grid), dim3(pa::kPrefixThreads), pa::PrefixSmem::kAlloc, stream, mk, mv, p);
+    st = launch(kernel, dim3(prefix_ctas), dim3(pa::kPrefixThreads), pa::PrefixSmem::kAlloc, stream, mk, mv, p);
     if (st != PA_OK) return st;
   }
   using SM = pa::DecodeSmem<T, G, Math>;
@@ -896,13 +922,13 @@ pa_status_t launch_prefix(const CUtensorMap &mk, const CUtensorMap &mv, const pa
 }
 
 template <typename T>
-pa_status_t dispatch_prefix(int group, const CUtensorMap &mk, const CUtensorMap &mv, const pa::PrefixParams &p,
-                            int num_groups, cudaStream_t s) {
+pa_status_t dispatch_prefix(int group, const CUtensorMap &mk, const CUtensorMap &mv, const pa::SuffixParams &p,
+                            unsigned prefix_ctas, cudaStream_t s) {
   switch (group) {
-    case 1: return launch_prefix<T, 1, pa::FmaMath<T, 1>>(mk, mv, p, num_groups, s);
-    case 2: return launch_prefix<T, 2, pa::MmaMath<T, 2>>(mk, mv, p, num_groups, s);
-    case 4: return launch_prefix<T, 4, pa::MmaMath<T, 4>>(mk, mv, p, num_groups, s);
-    case 8: return launch_prefix<T, 8, pa::MmaMath<T, 8>>(mk, mv, p, num_groups, s);
+    case 1: return launch_prefix<T, 1, pa::FmaMath<T, 1>>(mk, mv, p, prefix_ctas, s);
+    case 2: return launch_prefix<T, 2, pa::MmaMath<T, 2>>(mk, mv, p, prefix_ctas, s);
+    case 4: return launch_prefix<T, 4, pa::MmaMath<T, 4>>(mk, mv, p, prefix_ctas, s);
+    case 8: return launch_prefix<T, 8, pa::MmaMath<T, 8>>(mk, mv, p, prefix_ctas, s);
   }
   return PA_ERR_SHAPE;
 }
@@ -946,8 +972,8 @@ pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cach
     return PA_ERR_ALIGN;
   const PrefixPlan plan = plan_prefix(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, max_prefix_len,
                                       max_suffix_len, max_group_size);
-  // CTAs of the two launches (in floating point: a product of four counts may pass 2^63)
-  if ((double)num_groups * plan.row_ctas * num_kv_heads * plan.parts > INT32_MAX ||
+  // CTAs of the two launches (in floating point: a product of counts may pass 2^63)
+  if (plan.ctas > INT32_MAX ||
       (double)num_seqs * num_kv_heads * plan.suffix_parts > INT32_MAX)
     return PA_ERR_SHAPE;
   if (!workspace || workspace_bytes < plan.ws.bytes) return PA_ERR_WORKSPACE;
@@ -957,7 +983,7 @@ pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cach
       !encode_cache_map(&mv, v_cache, num_blocks, num_kv_heads, kRowBytes))
     return PA_ERR_CUDA;
   char *w = static_cast<char *>(workspace);
-  pa::PrefixParams p{};
+  pa::SuffixParams p{};
   p.out = out;
   p.q = q;
   p.block_tables = block_tables;
@@ -983,13 +1009,14 @@ pa_status_t pa_decode_shared_prefix(void *out, const void *q, const void *k_cach
   p.max_group_size = max_group_size;
   p.slots = plan.slots;
   p.slot0 = plan.slot0;
-  p.parts = plan.parts;
-  p.part_tokens = plan.part_tokens > 0 ? plan.part_tokens : pa::kPrefixKv;
-  p.row_ctas = plan.row_ctas;
+  p.levels = plan.levels;
+  p.most_row_ctas = plan.most_row_ctas;
+  std::copy(plan.part_tiles, plan.part_tiles + pa::kPrefixLevels, p.part_tiles);
+  const unsigned prefix_ctas = (unsigned)plan.ctas;
   const int group = num_heads / num_kv_heads;
   cudaStream_t s = (cudaStream_t)stream;
-  return dtype == PA_F16 ? dispatch_prefix<__half>(group, mk, mv, p, num_groups, s)
-                         : dispatch_prefix<__nv_bfloat16>(group, mk, mv, p, num_groups, s);
+  return dtype == PA_F16 ? dispatch_prefix<__half>(group, mk, mv, p, prefix_ctas, s)
+                         : dispatch_prefix<__nv_bfloat16>(group, mk, mv, p, prefix_ctas, s);
 }
 
 // ---------------------------------------------------------------- block-sparse decode

@@ -104,12 +104,19 @@ struct DecodeParams {
 constexpr int kWalkAll = 0, kWalkSuffix = 1, kWalkSelected = 2;
 constexpr int kJoinBatch = 8;   // kWalkSuffix: the prefix's partials in flight per thread when it combines
 
+constexpr int kPrefixRows = 128;          // rows of a warpgroup of the prefix kernel; a CTA has two
+constexpr int kPrefixKv = 128;            // tokens of its K/V tile
+constexpr int kPrefixLevels = 16;
+
 struct SuffixParams : DecodeParams {   // context_lens: whole lengths; max_context_len: of the suffix
   const int32_t *group_start;     // [num_groups + 1]
   const int32_t *prefix_lens;     // [num_groups]
   int num_groups, max_prefix_len, max_group_size;
-  int parts, part_tokens;         // partitions of the longest prefix (0: no prefix kernel); tokens of each
-  int slots, slot0;               // partials of a row in the workspace; the first of the suffix's
+  int slots, slot0;               // partials of a row in the workspace; the first of the suffix's (0: no prefix kernel)
+  // Tiles of a partition of a prefix, by the batch's work (prefix_part_tiles): level i is for at
+  // most ceil(most_row_ctas / 2^i) CTAs' rows over prefixes of max_prefix_len.
+  int levels, most_row_ctas;
+  int part_tiles[kPrefixLevels];
 };
 
 // Workspace rows of a (KV head, slot): the S * G (sequence, grouped head) rows, consecutive.
@@ -135,47 +142,91 @@ struct WalkParams<kWalkSelected> {
   using type = SelectedParams;
 };
 
-// The group that sequence b is in (sequences group_start[i] .. group_start[i+1]-1
-// are group i) and its prefix; called by whole warps, every lane with the same b.
-// ok = false if the group's entries are out of range (nothing is read with them).
-struct PrefixGroup {
-  int index, s0, s1, prefix;
-  bool ok;
-};
-
-__device__ __forceinline__ PrefixGroup group_of(const SuffixParams &p, int b) {
-  int n = 0;   // groups that start at or before b
-  for (int i0 = 0; i0 < p.num_groups; i0 += 32) {
-    const int i = i0 + (threadIdx.x & 31);
-    n += __popc(__ballot_sync(kFullMask, i < p.num_groups && p.group_start[i] <= b));
-  }
-  PrefixGroup r;
-  r.index = n - 1;
-  r.ok = n > 0;
-  r.s0 = r.s1 = r.prefix = 0;
-  if (r.ok) {
-    r.s0 = p.group_start[r.index];
-    r.s1 = p.group_start[r.index + 1];
-    r.prefix = p.prefix_lens[r.index];
-    r.ok = r.s0 >= 0 && r.s0 <= b && b < r.s1 && r.s1 <= p.num_seqs && r.s1 - r.s0 <= p.max_group_size &&
-           r.prefix >= 0 && r.prefix <= p.max_prefix_len && r.prefix % kBlockSize == 0 &&
-           r.prefix / kBlockSize <= p.max_blocks_per_seq;
-  }
-  return r;
-}
-
 // The CTA of the prefix kernel that has a group's rows row0 .. row0 + 255 runs as
 // "split" (its two warpgroups share the rows, and leave a partial each) if at most
 // 128 of them exist, else as "pair" (128 rows, one partial each).
-constexpr int kPrefixRows = 128;
 __device__ __forceinline__ bool prefix_split(int rows_in_group, int row_cta) {
   return rows_in_group - row_cta * 2 * kPrefixRows <= kPrefixRows;
 }
 
+// Group i is sequences group_start[i] .. group_start[i+1]-1 and their prefix.  ok = false if
+// its entries are out of range (nothing is read with them).
+struct PrefixGroup {
+  int index, s0, s1, prefix;
+  bool ok;
+  // what it asks of the prefix kernel: CTAs' rows (0: nothing) and tiles
+  template <int G>
+  __device__ __forceinline__ int row_ctas() const {
+    return ok && prefix > 0 ? ((s1 - s0) * G + 2 * kPrefixRows - 1) / (2 * kPrefixRows) : 0;
+  }
+  __device__ __forceinline__ int tiles() const { return (prefix + kPrefixKv - 1) / kPrefixKv; }
+};
+
+__device__ __forceinline__ PrefixGroup prefix_group(const SuffixParams &p, int i) {   // i < 0: none
+  PrefixGroup r{i, 0, 0, 0, false};
+  if (i < 0) return r;
+  r.s0 = p.group_start[i];
+  r.s1 = p.group_start[i + 1];
+  r.prefix = p.prefix_lens[i];
+  r.ok = r.s0 >= 0 && r.s1 >= r.s0 && r.s1 <= p.num_seqs && r.s1 - r.s0 <= p.max_group_size && r.prefix >= 0 &&
+         r.prefix <= p.max_prefix_len && r.prefix % kBlockSize == 0 && r.prefix / kBlockSize <= p.max_blocks_per_seq;
+  return r;
+}
+
+// Group 32 * turn + lane; where all groups are one turn, lanes keep theirs.
+__device__ __forceinline__ PrefixGroup lane_group(const SuffixParams &p, int i0) {
+  const int i = i0 + (threadIdx.x & 31);
+  PrefixGroup r{i, 0, 0, 0, true};   // past the last one: empty
+  return i < p.num_groups ? prefix_group(p, i) : r;
+}
+
+// Tiles of a partition of the prefixes: that of the last level whose rows hold the batch's
+// work, the sum of (CTAs' rows x tiles) over its groups.  The host knows only the largest
+// group and the longest prefix; planned for a batch of those, one group of 64 over 32768
+// tokens beside 50 sequences without a prefix was left whole, 8 CTAs of 256 tiles
+// (751 us a call; 98 with this sum).  (It fits 32 bits: the host sees to it.)
+__device__ __forceinline__ int part_tiles_for(const SuffixParams &p, unsigned work) {
+  const unsigned most_tiles = (p.max_prefix_len + kPrefixKv - 1) / kPrefixKv;
+  int level = p.levels - 1;
+  while (level > 0 && ((p.most_row_ctas + (1u << level) - 1) >> level) * most_tiles < work) --level;
+  return p.part_tiles[level];
+}
+
+// The batch's work.  By whole warps, as group_of.
+template <int G>
+__device__ __forceinline__ unsigned prefix_work(const SuffixParams &p) {
+  if (p.levels == 1) return 0;   // (nothing to choose)
+  unsigned work = 0;
+  for (int i0 = 0; i0 < p.num_groups; i0 += 32) {
+    const PrefixGroup e = lane_group(p, i0);
+    work += static_cast<unsigned>(e.row_ctas<G>()) * e.tiles();
+  }
+  return __reduce_add_sync(kFullMask, work);
+}
+
+// The group that sequence b (the same in every lane) is in.
+__device__ __forceinline__ PrefixGroup group_of(const SuffixParams &p, int b) {
+  PrefixGroup r{};
+  if (p.num_groups == 1) {
+    r = prefix_group(p, 0);
+    if (r.s0 > b) r.index = -1;
+  } else {
+    int n = 0;   // groups that start at or before b
+    for (int i0 = 0; i0 < p.num_groups; i0 += 32) {
+      const int i = i0 + (threadIdx.x & 31);
+      n += __popc(__ballot_sync(kFullMask, i < p.num_groups && p.group_start[i] <= b));
+    }
+    r = prefix_group(p, n - 1);
+  }
+  r.ok = r.ok && r.s0 <= b && b < r.s1;
+  return r;
+}
+
 // How many partials of the prefix the row of sequence b and grouped head hh has.
 template <int G>
-__device__ __forceinline__ int prefix_partials(const SuffixParams &p, const PrefixGroup &group, int b, int hh) {
-  const int parts = (group.prefix + p.part_tokens - 1) / p.part_tokens;
+__device__ __forceinline__ int prefix_partials(const PrefixGroup &group, int part_tiles, int b, int hh) {
+  const int tiles = group.tiles();
+  const int parts = tiles > 0 ? (tiles + part_tiles - 1) / part_tiles : 0;
   const int row = (b - group.s0) * G + hh;
   return prefix_split((group.s1 - group.s0) * G, row / (2 * kPrefixRows)) ? 2 * parts : parts;
 }
@@ -825,7 +876,7 @@ struct WaitAtExit {   // pdl_wait() on every way out of the kernel
 
 template <int kWalk>
 __device__ __forceinline__ bool waits_late(const typename WalkParams<kWalk>::type &p) {
-  if constexpr (kWalk == kWalkSuffix) return p.parts > 0;
+  if constexpr (kWalk == kWalkSuffix) return p.slot0 > 0;
   return false;
 }
 
@@ -980,6 +1031,10 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
 
   Math math;
   math.init(scratch, qg, p.scale_log2, warp, lane);
+  int part_tiles = 1;   // of the prefix (looked up while the first tiles are on their way)
+  if constexpr (kWalk == kWalkSuffix) {
+    if (late && joins) part_tiles = part_tiles_for(p, prefix_work<G>(p));
+  }
 
   bool ok = true;
   int j = 0;
@@ -1071,7 +1126,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
         continue;
       }
       pdl_wait();   // the prefix's partials are visible from here on
-      const int na = prefix_partials<G>(p, group, b, hh);
+      const int na = prefix_partials<G>(group, part_tiles, b, hh);
       for (int k0 = 0; k0 < na; k0 += kJoinBatch) {
         float mk[kJoinBatch], lk[kJoinBatch];
         float4 x[kJoinBatch];

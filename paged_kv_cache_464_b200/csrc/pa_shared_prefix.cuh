@@ -55,16 +55,75 @@
 
 namespace pa {
 
-constexpr int kPrefixKv = 128;            // tokens of a K/V tile
 constexpr int kPrefixThreads = 384;
 constexpr int kPrefixMmaWarp = 8;
 constexpr int kPrefixLoadWarp = 10;
 constexpr int kPrefixStagesPair = 5;      // one ring
 constexpr int kPrefixStagesSplit = 3;     // each of two rings
 
-struct PrefixParams : SuffixParams {
-  int row_ctas;             // CTAs of 256 rows a (group, KV head, partition)
+// Which part of the batch's work CTA blockIdx.x has.  The items of a group, ((256 rows) x KV
+// head) x partition with the partitions of the same rows side by side, follow those of
+// the groups before it; groups without a prefix have none, so that idle CTAs come last.
+// By whole warps.
+struct PrefixItem {
+  int s0, s1, prefix, part_tiles, row_cta, head, part;
+  bool some;   // false: past the last item
 };
+
+template <int G>
+__device__ __forceinline__ PrefixItem prefix_item(const SuffixParams &p) {
+  PrefixItem r{};
+  if (p.num_groups == 1) {   // the longest prefix's partitions, as the grid has them
+    const int parts = p.slot0 / 2, rows = blockIdx.x / parts;
+    r.part = blockIdx.x % parts;
+    r.head = rows % p.num_kv_heads;
+    r.row_cta = rows / p.num_kv_heads;
+    r.part_tiles = p.part_tiles[0];
+    const PrefixGroup e = prefix_group(p, 0);
+    if (!e.ok && blockIdx.x == 0 && threadIdx.x == 0) record_error(8 /*PA_DEV_BAD_GROUP*/, 0);
+    r.s0 = e.s0;
+    r.s1 = e.s1;
+    r.prefix = e.prefix;
+    r.some = e.ok && r.row_cta * 2 * kPrefixRows < (e.s1 - e.s0) * G && r.part * r.part_tiles < e.tiles();
+    return r;
+  }
+  const int lane = threadIdx.x & 31;
+  PrefixGroup e = lane_group(p, 0);
+  r.part_tiles = part_tiles_for(
+      p, p.num_groups > 32 ? prefix_work<G>(p)
+                           : __reduce_add_sync(kFullMask, static_cast<unsigned>(e.row_ctas<G>()) * e.tiles()));
+  int at = blockIdx.x;   // counted from the items of these 32 groups
+  for (int i0 = 0;;) {
+    if (!e.ok && blockIdx.x == 0 && threadIdx.x < 32) record_error(8 /*PA_DEV_BAD_GROUP*/, e.index);
+    const int row_ctas = e.row_ctas<G>();
+    const int parts = e.ok ? (e.tiles() + r.part_tiles - 1) / r.part_tiles : 0;
+    const int items = row_ctas * p.num_kv_heads * parts;
+    int upto = items;   // of lanes 0 .. lane
+    for (int off = 1; off < 32 && off < p.num_groups; off <<= 1) {
+      const int y = __shfl_up_sync(kFullMask, upto, off);
+      if (lane >= off) upto += y;
+    }
+    const unsigned here = __ballot_sync(kFullMask, at < upto);
+    if (here != 0u && !r.some) {   // the first such lane's group has item `at`
+      const int src = __ffs(here) - 1;
+      const int k = __shfl_sync(kFullMask, at - (upto - items), src);
+      const int n = __shfl_sync(kFullMask, parts, src);
+      r.s0 = __shfl_sync(kFullMask, e.s0, src);
+      r.s1 = __shfl_sync(kFullMask, e.s1, src);
+      r.prefix = __shfl_sync(kFullMask, e.prefix, src);
+      const int rows = k / max(n, 1);
+      r.part = k % max(n, 1);
+      r.head = rows % p.num_kv_heads;
+      r.row_cta = rows / p.num_kv_heads;
+      // (not so only where overlapping groups, which are reported, have more items than 32 bits count)
+      r.some = k >= 0 && n > 0 && r.row_cta < __shfl_sync(kFullMask, row_ctas, src);
+    }
+    // CTA 0 looks at every group, to report bad ones
+    if ((i0 += 32) >= p.num_groups || (r.some && blockIdx.x != 0)) return r;
+    at -= __shfl_sync(kFullMask, upto, 31);
+    e = lane_group(p, i0);
+  }
+}
 
 struct PrefixSmem {
   static constexpr int kTile = 128 * 256;                  // [2 halves][128 rows][128 B]
@@ -203,7 +262,7 @@ __device__ __forceinline__ void exp_chunk(uint32_t taddr, int live, float2 cc2, 
 template <typename T, int G>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     pa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                            const PrefixParams p) {
+                            const SuffixParams p) {
   using SM = PrefixSmem;
   using PK = Pack16<T>;
   constexpr int D = 128;
@@ -230,26 +289,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // ---- work item: blockIdx.x = ((group * row_ctas + rc) * Hkv + g) * parts + part
-  int item = blockIdx.x;
-  const int part = item % p.parts;
-  item /= p.parts;
-  const int g = item % p.num_kv_heads;
-  item /= p.num_kv_heads;
-  const int rc = item % p.row_ctas;
-  const int group = item / p.row_ctas;
-  const int s0 = p.group_start[group], s1 = p.group_start[group + 1];
-  const int prefix = p.prefix_lens[group];
-  if (s0 < 0 || s1 < s0 || s1 > p.num_seqs || s1 - s0 > p.max_group_size || prefix < 0 || prefix > p.max_prefix_len ||
-      prefix % kBlockSize != 0 || prefix / kBlockSize > p.max_blocks_per_seq) {
-    if (part == 0 && g == 0 && rc == 0 && tid == 0) record_error(8 /*PA_DEV_BAD_GROUP*/, group);
-    return;
-  }
+  const PrefixItem item = prefix_item<G>(p);
+  if (!item.some) return;
+  const int s0 = item.s0, s1 = item.s1, prefix = item.prefix;
+  const int g = item.head, rc = item.row_cta, part = item.part;
   const int rows_group = (s1 - s0) * G;
   const int row0 = rc * 2 * kPrefixRows;
-  const int tok0 = part * p.part_tokens;
-  if (row0 >= rows_group || tok0 >= prefix) return;
-  const int tokens = min(p.part_tokens, prefix - tok0);
+  const int part_tokens = item.part_tiles * kPrefixKv;
+  const int tok0 = part * part_tokens;
+  const int tokens = min(part_tokens, prefix - tok0);
   const int ntiles = (tokens + kPrefixKv - 1) / kPrefixKv;
   const int nblk = tokens / kBlockSize;
   const bool split = prefix_split(rows_group, rc);
@@ -566,11 +614,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 // Join of a row's prefix partials (slots 0 ..) and those of its own tokens (slot0 ..):
 // only where the own tokens are more than one partition (else the suffix walk does it).
 template <typename T, int G>
-__global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const SuffixParams p) {
   pdl_wait();
   pdl_trigger();
   const long long rows = static_cast<long long>(p.num_seqs) * p.num_heads;
   const long long step = static_cast<long long>(gridDim.x) * kReduceWarps;
+  const int part_tiles = p.slot0 > 0 ? part_tiles_for(p, prefix_work<G>(p)) : 1;
   for (long long row = static_cast<long long>(blockIdx.x) * kReduceWarps + (threadIdx.x >> 5); row < rows; row += step) {
     const int b = static_cast<int>(row / p.num_heads);
     const int h = static_cast<int>(row % p.num_heads);
@@ -579,7 +628,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_join_shared_kernel(const
     if (!group.ok || L < group.prefix || L - group.prefix > p.max_context_len || L > p.max_blocks_per_seq * kBlockSize)
       continue;   // recorded by the partition kernel; the row is left as it was
     join_row<T>(p, row, prefix_slot(p, h / G, 0) + static_cast<size_t>(b) * G + h % G,
-                static_cast<size_t>(p.num_seqs) * G, prefix_partials<G>(p, group, b, h % G), p.slot0,
+                static_cast<size_t>(p.num_seqs) * G, prefix_partials<G>(group, part_tiles, b, h % G), p.slot0,
                 (L - group.prefix + p.partition_size - 1) / p.partition_size);
   }
 }

@@ -264,3 +264,62 @@ def test_weights_of_two_kinds_that_nearly_cancel(pa, ty, bits, size):
     # and sums of 2048 products over 16 steps of 128 tokens each: below 2^-18 together
     tol = ref.HALF_STEP[ty] * want.abs() + (2.0 ** -bits + 2.0 ** -18) * weight + 2.0 ** -25
     assert ((out.double() - want).abs() <= tol).all(), ((out.double() - want).abs() / weight).max()
+
+
+@pytest.mark.parametrize("at", [0, 1, 31, 32, 40, 65])
+def test_one_long_prefix_among_many_groups(pa, at):
+    """The group with the prefix stands anywhere among sequences that share nothing, some groups empty."""
+    sizes = [i % 3 % 2 for i in range(66)]
+    prefixes = [0] * 66
+    sizes[at], prefixes[at] = 37, 4000
+    sizes[50], prefixes[50] = 5, 272
+    check(pa, sizes, prefixes, lambda b: 1 + (13 * b) % 60, 2, 4, "bf16", seed=20 + at)
+
+
+@pytest.mark.parametrize("G,ty", [(1, "f16"), (8, "bf16")])
+def test_groups_of_every_kind(pa, G, ty):
+    """More and fewer rows than a CTA takes, long and short prefixes, split suffixes in one of them (a third launch)."""
+    sizes, prefixes = [70, 1, 300 // G, 0, 2, 33], [640, 3008, 144, 512, 0, 1040]
+    check(pa, sizes, prefixes, lambda b: 2 + b % 30, 1, G, ty, seed=30)
+    check(pa, sizes, prefixes, lambda b: 1100 if b == 73 else 2 + b % 30, 1, G, ty, seed=31)
+
+
+def test_groups_without_a_prefix_leave_the_split_of_the_others(pa):
+    """A group of 64 over a long prefix, alone and beside 50 sequences that share nothing: the added rows' own work is
+    small, so the call must not take several times as long (nine times, when every group was planned as a long one)."""
+    prefix, hq, hkv = 32768, 32, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    blocks = prefix // 16
+    k = torch.randn((blocks + 114 * 8, 16, hkv, 128), generator=g, device="cuda").bfloat16()
+    v = torch.randn(k.shape, generator=g, device="cuda").bfloat16()
+    q = torch.randn((114, hq, 128), generator=g, device="cuda").bfloat16()
+    tables = torch.zeros((114, blocks + 8), dtype=torch.int32, device="cuda")
+    tables[:64, :blocks] = torch.randperm(blocks, generator=g, device="cuda").int()
+    own = blocks + torch.arange(114 * 8, device="cuda").int().view(114, 8)
+    tables[:64, blocks:], tables[64:, :8] = own[:64], own[64:]
+    lens = torch.tensor([prefix + 100] * 64 + [120] * 50, dtype=torch.int32, device="cuda")
+
+    def run(n):
+        gs = torch.tensor([0] + list(range(64, n + 1)), dtype=torch.int32, device="cuda")
+        pl = torch.tensor([prefix] + [0] * (n - 64), dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q[:n])
+        need = pa.decode_shared_prefix_workspace_bytes(n, n - 63, hq, hkv, 128, prefix, 120, 64)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        best = 1e9
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(200_000)      # the call's host side passes behind it
+            a.record()
+            pa.decode_shared_prefix(q[:n], k, v, tables[:n], lens[:n], gs, pl, 0.088, out, max_prefix_len=prefix,
+                                    max_suffix_len=120, max_group_size=64, workspace=ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return out, best
+
+    alone, t_alone = run(64)
+    mixed, t_mixed = run(114)
+    assert ((alone.float() - mixed[:64].float()).abs() <= 2.0 ** -12 + 2.0 ** -7 * alone.float().abs()).all()
+    rest = pa.decode(q[64:], k, v, tables[64:], lens[64:], 0.088, max_context_len=120)
+    assert ((mixed[64:].float() - rest.float()).abs() <= 2.0 ** -12 + 2.0 ** -7 * rest.float().abs()).all()
+    assert t_mixed < 2.5 * t_alone, (t_mixed, t_alone)

@@ -203,3 +203,12 @@ def test_binding_refuses_host_tensors(capi):
 def test_stall_hook_takes_the_prefix_kernel(capi):
     assert capi.raw.pa_test_stall_next_launch(3, -1) == 0
     assert capi.raw.pa_test_stall_next_launch(4, 0) == SHAPE
+
+
+def test_shared_prefix_plan_of_a_mixed_batch(capi):
+    """Sequences that share nothing (groups of one without a prefix) leave a long prefix its partitions: the workspace
+    has room for a group's partials as if it were alone.  (Its rows' share grows with the batch, so fewer may be best.)"""
+    size = capi.decode_shared_prefix_workspace_bytes
+    alone = size(64, 1, 32, 8, 128, 32768, 512, 64) / 64
+    for n in (1, 8, 20, 50):
+        assert size(64 + n, 1 + n, 32, 8, 128, 32768, 512, 64) / (64 + n) >= 0.6 * alone
