@@ -150,7 +150,9 @@ pa_status_t pa_rope_table(float *cos_sin, int max_position, int rotary_dim, doub
  *               value may be slices of one projection's output; key, value
  *               likewise with num_kv_heads; q_out likewise.  All in dtype.
  *               q_out may be q itself (same pointer and stride: rotated in
- *               place); otherwise it must not overlap q, key or value.
+ *               place), or other columns of the rows that hold an input (with
+ *               the input's stride); otherwise the memory from its first to its
+ *               last element must not overlap that of q, key or value.
  * positions     [num_tokens] int64.  A token with position < 0 is padding: its
  *               rows may be read, and nothing is written for it.  position >= max_position: the
  *               token is skipped and recorded as PA_DEV_BAD_POSITION.

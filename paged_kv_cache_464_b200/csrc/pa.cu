@@ -681,6 +681,17 @@ bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes
   return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Do n rows of a_row bytes, a_stride apart, and n of b_row bytes overlap?  Rows as far
+// apart as each other (columns of the same wider rows) are compared as such, others by
+// the ranges they span.
+bool rows_overlap(const void *a, size_t a_stride, size_t a_row, const void *b, size_t b_stride, size_t b_row, int n) {
+  if (!ranges_overlap(a, (n - 1) * a_stride + a_row, b, (n - 1) * b_stride + b_row)) return false;
+  if (a_stride != b_stride) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t after = y >= x ? (y - x) % a_stride : (a_stride - (x - y) % a_stride) % a_stride;
+  return after < a_row || after + b_row > a_stride;   // b's columns start within a's, or run into the next row's
+}
+
 // Heads a thread: three where that leaves a wave of CTAs (256 threads, up to eight an
 // SM), one below that, where the number of CTAs counts more.
 template <typename T>
@@ -726,11 +737,11 @@ pa_status_t rope_impl(void *q_out, const void *q, const void *key, const void *v
       !aligned(v_cache, 16) || !aligned(cos_sin, 16) || !aligned(positions, 8) || !aligned(slot_mapping, 8) ||
       q_stride % epc != 0 || q_out_stride % epc != 0 || k_stride % epc != 0 || v_stride % epc != 0)
     return PA_ERR_ALIGN;
-  auto span = [&](int64_t stride, int64_t row) { return (size_t)((num_tokens - 1) * stride + row) * es; };
+  auto meets = [&](const void *x, int64_t x_stride, int64_t x_row) {
+    return rows_overlap(q_out, q_out_stride * es, q_row * es, x, x_stride * es, x_row * es, num_tokens);
+  };
   if (!(q_out == q && q_out_stride == q_stride) &&
-      (ranges_overlap(q_out, span(q_out_stride, q_row), q, span(q_stride, q_row)) ||
-       ranges_overlap(q_out, span(q_out_stride, q_row), key, span(k_stride, kv_row)) ||
-       ranges_overlap(q_out, span(q_out_stride, q_row), value, span(v_stride, kv_row))))
+      (meets(q, q_stride, q_row) || meets(key, k_stride, kv_row) || meets(value, v_stride, kv_row)))
     return PA_ERR_SHAPE;
   pa::RopeParams p{};
   p.q_out = q_out;

@@ -265,3 +265,31 @@ def test_binding_refusals(pa):
         call(out=dev[:, 1:3])        # overlaps q
     with pytest.raises(pa.PaError):
         call(table=torch.zeros((8, 24), device="cuda"))
+
+
+@pytest.mark.parametrize("order", ["oqkv", "qkvo", "qokv"])
+@pytest.mark.parametrize("T", [1, 2, 37])
+def test_rotated_q_beside_its_inputs(pa, order, T):
+    """q_out as other columns of the buffer that holds q, key and value: slices of the same rows, none in common."""
+    hq, hkv, d = 8, 2, 128
+    qkv, pos, slot, blocks = make(T, hq, hkv, "bf16", d, 256, seed=T)
+    heads = {"q": hq, "k": hkv, "v": hkv, "o": hq}
+    at, wide = {}, torch.full((T, 2 * hq + 2 * hkv, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    n = 0
+    for name in order:
+        at[name] = wide[:, n:n + heads[name]]
+        n += heads[name]
+    for name, part in (("q", qkv[:, :hq]), ("k", qkv[:, hq:hq + hkv]), ("v", qkv[:, hq + hkv:])):
+        at[name].copy_(part)
+    table = pa.rope_table(256, d)
+    kc = torch.zeros((blocks, 16, hkv, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    pa.rope_and_cache(at["q"], at["k"], at["v"], pos.cuda(), table, kc, vc, slot.cuda(), at["o"])
+    assert torch.equal(at["o"].cpu(), plain_fp32(qkv[:, :hq], pos, table.cpu(), False).bfloat16())
+    assert torch.equal(torch.cat([at["q"], at["k"], at["v"]], 1).cpu(), qkv)
+    assert torch.equal(vc.view(-1, hkv, d)[slot.cuda()].cpu(), qkv[:, hq + hkv:])
+    first = sum(heads[c] for c in order[:order.index("q")])
+    for lo in (first - hq + 1, first + hq - 1):      # a head in common with q
+        if 0 <= lo and lo + hq <= wide.shape[1]:
+            with pytest.raises(pa.PaError):
+                pa.rope_and_cache(at["q"], at["k"], at["v"], pos.cuda(), table, kc, vc, slot.cuda(), wide[:, lo:lo + hq])

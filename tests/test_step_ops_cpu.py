@@ -212,3 +212,18 @@ def test_shared_prefix_plan_of_a_mixed_batch(capi):
     alone = size(64, 1, 32, 8, 128, 32768, 512, 64) / 64
     for n in (1, 8, 20, 50):
         assert size(64 + n, 1 + n, 32, 8, 128, 32768, 512, 64) / (64 + n) >= 0.6 * alone
+
+
+def test_rope_refuses_rows_that_share_columns(capi):
+    """q_out in the same wide rows as q, key and value (rows of 1024, 256 and 256 elements, 2560 apart): any element in
+    common, in the same row or a neighbouring one, is refused."""
+    wide, row, kv = 2560 * 2, 1024 * 2, 256 * 2
+    a = dict(so=2560, sq=2560, sk=2560, sv=2560, T=4, q=BIG, key=BIG + row, val=BIG + row + kv)
+    for shift in (16, row - 16, 16 - row):
+        for turn in (-wide, 0, wide):
+            assert _rope(capi, **a, qo=BIG + shift + turn) == SHAPE, (shift, turn)
+    free = row + 2 * kv                                   # the columns behind value
+    for shift in (-16, 16):                               # into value, and around into the next row's q
+        assert _rope(capi, **a, qo=BIG + free + shift) == SHAPE, shift
+    # other strides are compared as whole ranges
+    assert _rope(capi, **{**a, "so": 5120}, qo=BIG + free) == SHAPE
