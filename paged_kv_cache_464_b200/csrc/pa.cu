@@ -90,7 +90,8 @@ pa_status_t cache_shape_status(int64_t num_blocks, int block_size, int num_kv_he
 
 // Every kernel is launched with programmatic stream serialisation: it may be
 // scheduled while the previous kernel in the stream is still running, and it
-// waits (griddepcontrol.wait) before touching global memory, so stream order
+// waits (griddepcontrol.wait) before touching global memory (but for the suffix
+// walk of a shared prefix: pa_common.cuh, launch ordering), so stream order
 // semantics are unchanged while the launch latency overlaps the previous tail.
 template <typename... KArgs, typename... Args>
 pa_status_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

@@ -164,7 +164,12 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // in the stream may start before this one ends.  Each kernel calls pdl_wait()
 // before its first global-memory access (it returns once the previous grid in
 // the stream has completed and its writes are visible; a no-op when launched
-// without the attribute), and pdl_trigger() to let its successor launch.
+// without the attribute), and only then pdl_trigger(), to let its successor launch:
+// what starts after that has everything from before this kernel.  One grid relies on
+// that order: the suffix walk behind the shared-prefix kernel (pa_decode.cuh,
+// kWalkSuffix) reads its inputs and writes its partials without waiting.  Its last
+// CTA waits on every way out, so that the grid still ends after the one before it.
+// A kernel that triggers before it waits must not be launched directly before it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -975,6 +975,7 @@ __global__ void __launch_bounds__(W * 32, decode_min_ctas(W))
   int my_id = -1;      // lane l holds the physical id of j = 32 * id_group + l
   int my_valid = 0;    // kWalkSelected: and how many of its tokens count (0 = no block)
   uint32_t stage_valid = 0;   // kWalkSelected: the counts of the blocks in flight, 8 bits a stage
+  static_assert(kWalk != kWalkSelected || kSPW <= 4, "a stage's count is 8 of 32 bits");
   const uint64_t policy = policy_evict_first();
 
   auto issue = [&](int j) {   // called by all 32 lanes, j warp-uniform
