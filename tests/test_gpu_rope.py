@@ -293,3 +293,41 @@ def test_rotated_q_beside_its_inputs(pa, order, T):
         if 0 <= lo and lo + hq <= wide.shape[1]:
             with pytest.raises(pa.PaError):
                 pa.rope_and_cache(at["q"], at["k"], at["v"], pos.cuda(), table, kc, vc, slot.cuda(), wide[:, lo:lo + hq])
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (30, 3), (4, 20)])
+def test_large_batches(pa, ty, interleaved, hq, hkv):
+    """More than a wave of CTAs: three heads a thread, with a last one that 36, 44 or 48 rows leave in part without."""
+    T, d = 2999, ref.HEAD_DIM[ty]
+    part = 2 if hq == 30 else 1
+    qkv, pos, slot, blocks = make(T, hq, hkv, ty, d // part, 5000, seed=hq, padding=[0, 1501, 2998])
+    table = pa.rope_table(5000, d // part, 10000.0)
+    dev, pos, slot = qkv.cuda(), pos.cuda(), slot.cuda()
+    q, k, v = dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:]
+    live = pos >= 0
+    want_q, want_k = (plain_fp32(x, pos, table, interleaved) for x in (q, k))    # (elementary operations, on the device)
+
+    def caches(dtype):
+        kc = torch.full((blocks, 16, hkv, d), 7.0, device="cuda").to(dtype)
+        return kc, kc.clone()
+
+    kinds = ["same"] if ty == "f32" else ["same", "fp8"]
+    for kind in kinds:
+        kc, vc = caches(torch.float8_e4m3fn if kind == "fp8" else dev.dtype)
+        q_out = torch.full((T, hq, d), 3.0, dtype=dev.dtype, device="cuda")
+        if kind == "fp8":
+            pa.rope_and_cache_fp8(q, k, v, pos, table, kc, vc, slot, 0.0125, 0.02, q_out, interleaved=interleaved)
+            # (by a tensor: torch divides a CUDA tensor by a number as a product with its reciprocal)
+            rows_k = (want_k / torch.full_like(want_k, 0.0125)).clamp(-448, 448).to(kc.dtype)
+            rows_v = (v.float() / torch.full_like(v.float(), 0.02)).clamp(-448, 448).to(kc.dtype)
+        else:
+            pa.rope_and_cache(q, k, v, pos, table, kc, vc, slot, q_out, interleaved=interleaved)
+            rows_k, rows_v = want_k.to(dev.dtype), v
+        rows_q = torch.where(live[:, None, None], want_q.to(dev.dtype), torch.full_like(q_out, 3.0))
+        assert torch.equal(q_out, rows_q)
+        for cache, rows in ((kc, rows_k), (vc, rows_v)):
+            want = caches(cache.dtype)[0].view(torch.uint8).view(-1, hkv, d * cache.element_size())
+            want[slot[live]] = rows[live].contiguous().view(torch.uint8)
+            assert torch.equal(cache.view(torch.uint8).view(want.shape), want)

@@ -351,3 +351,63 @@ def test_blocks_past_four_gigabytes(pa):
     out = pa.decode_selected(qd, k, v, fd, ld, chosen, 0.088)
     want, weight = ref.attention(q, ks, vs, tables, lens, 0.088, chosen.cpu())
     assert ((out.cpu().double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 16)).all()
+
+
+@pytest.mark.parametrize("ty,hkv,G,S,K", [("bf16", 8, 2, 64, 9), ("f16", 8, 4, 64, 21), ("bf16", 8, 8, 61, 33),
+                                          ("f16", 3, 8, 100, 70), ("bf16", 3, 4, 100, 70), ("f32", 8, 2, 64, 9)])
+def test_decode_of_large_batches(pa, ty, hkv, G, S, K):
+    """More CTAs than a wave of four-warp ones: two-warp CTAs for 16-bit grouped heads; lists with holes, of every
+    length from none, whole and in partitions that are joined (100 sequences of 3 heads)."""
+    g = torch.Generator().manual_seed(S + K)
+    lens = [0, 1, 16, 17] + [int(x) for x in torch.randint(1, 1200, (S - 4,), generator=g)]
+    k, v, tables, lens = ref.make_cache(lens, hkv, ty, seed=K)
+    q = ref.make_q(S, hkv * G, ty, seed=K)
+    chosen = torch.full((S, hkv, K), -1, dtype=torch.int32)
+    for b in range(S):
+        n = -(-int(lens[b]) // 16)
+        for h in range(hkv):
+            m = min(n, int(torch.randint(0, K + 1, (1,), generator=g)))
+            at = torch.randperm(K, generator=g)[:m]
+            chosen[b, h, at] = torch.randperm(n, generator=g)[:m].int()
+    scale = q.shape[2] ** -0.5
+    want, weight = ref.attention(q, k, v, tables, lens, scale, chosen)
+    out = torch.full_like(q, 4.0).cuda()
+    args = cuda(q, k, v, tables, lens, chosen)
+    pa.decode_selected(*args, scale, out)
+    err = (out.cpu().double() - want).abs()
+    tol = ref.attention_tolerance(want, weight, ty, 16)
+    assert (err <= tol).all(), (err - tol).max()
+    empty = ((chosen >= 0).sum(2) == 0).repeat_interleave(G, 1)
+    assert (out.cpu()[empty] == 0).all()
+    assert torch.equal(pa.decode_selected(*args, scale), out)
+
+
+@pytest.mark.parametrize("ty,G", [("bf16", 8), ("f16", 1), ("f32", 2)])
+@pytest.mark.parametrize("K,sink,recent", [(64, 1, 4), (520, 0, 0)])
+def test_choice_of_many_long_lists(pa, ty, G, K, sink, recent):
+    """More than two lists an SM: 256 threads a list, with blocks in registers (512), in shared memory (4096) and read
+    again behind those.  Blocks are drawn from 3000, so that ties are frequent."""
+    S, hkv, d, pool = 40, 8, ref.HEAD_DIM[ty], 3000
+    g = torch.Generator(device="cuda").manual_seed(K + G)
+    blocks = [0, 1, K, K + 1, 511, 512, 513, 600, 1025, 4095, 4096, 4097, 4099, 4607, 4608, 4609, 5000, 9000] + \
+        [400 + 37 * i for i in range(S - 18)]
+    lens = torch.tensor([max(0, 16 * n - n % 16) for n in blocks], dtype=torch.int32, device="cuda")
+    n = (lens + 15) // 16
+    tables = torch.randint(0, pool, (S, 9001), generator=g, device="cuda").int()
+    x = torch.randn((pool, 2, hkv, d), generator=g, device="cuda").to(ref.TYPES[ty])
+    bounds = torch.stack([x.amin(1), x.amax(1)], 1)
+    q = torch.randn((S, hkv * G, d), generator=g, device="cuda").to(ref.TYPES[ty])
+    got = pa.select_blocks(q, bounds, tables, lens, K, sink_blocks=sink, recent_blocks=recent)
+    rows = q.double().view(S, hkv, G, d)
+    score = (torch.einsum("bhgd,phd->bhgp", rows.clamp(min=0), bounds[:, 1].double())
+             + torch.einsum("bhgd,phd->bhgp", rows.clamp(max=0), bounds[:, 0].double())).amax(2)
+    for b in range(S):
+        m = int(n[b])
+        want = torch.full((hkv, K), -1, dtype=torch.int32, device="cuda")
+        if m:
+            s = score[b][:, tables[b, :m].long()].clone()     # the same block has the same score: ties are exact
+            s[:, :sink] = float("inf")
+            s[:, m - recent:] = float("inf") if recent else s[:, m:]
+            best = torch.sort(s, dim=1, descending=True, stable=True).indices[:, :K].sort(1).values
+            want[:, :best.shape[1]] = best.int()
+        assert torch.equal(got[b], want), b
