@@ -184,3 +184,85 @@ def test_sizes_of_nothing(pa):
     chosen = pa.select_blocks(q, b, t, i32, 3)
     assert chosen.shape == (0, 1, 3)
     assert pa.decode_selected(q, k, k, t, i32, chosen, 0.1).shape == q.shape
+
+
+class LongPrefix:
+    """480 rows over 65536 tokens of one KV head, and one sequence with 1100 tokens of its own: the walk over the
+    sequences' own tokens is split (a third launch joins), runs on the SMs that the prefix kernel leaves, and is
+    through long before it."""
+
+    def __init__(self, seed):
+        n, prefix = 60, 65536
+        lens = [prefix + (1100 if b == 17 else b % 7) for b in range(n)]
+        self.k, self.v, self.tables, self.lens = ref.make_cache(lens, 1, "bf16", seed=seed, shared=[(0, n, prefix)])
+        self.q = [ref.make_q(n, 8, "bf16", seed=seed + i) for i in range(2)]
+        self.device = [t.cuda() for t in (self.k, self.v, self.tables, self.lens)]
+        self.groups = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [prefix])]
+        self.q_device = [x.cuda() for x in self.q]
+
+    def call(self, pa, i, out, workspace):
+        return pa.decode_shared_prefix(self.q_device[i], *self.device, *self.groups, 0.088, out, max_prefix_len=65536,
+                                       max_suffix_len=1100, max_group_size=60, workspace=workspace)
+
+
+@pytest.fixture(scope="module")
+def long_prefix():
+    return LongPrefix(1)
+
+
+def test_prefix_that_outlasts_the_suffix_walk(pa, long_prefix):
+    """Calls one after the other with one workspace, eager and replayed: each gives what it gives alone."""
+    x = long_prefix
+    need = pa.decode_shared_prefix_workspace_bytes(60, 1, 8, 1, 128, 65536, 1100, 60)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    alone = []
+    for i in range(2):
+        ws.fill_(0xFF)      # NaN in every partial
+        alone.append(torch.empty_like(x.q_device[i]))
+        torch.cuda.synchronize()
+        x.call(pa, i, alone[i], ws)
+        torch.cuda.synchronize()
+        want, weight = ref.attention(x.q[i], x.k, x.v, x.tables, x.lens, 0.088)
+        assert ((alone[i].cpu().double() - want).abs() <= ref.attention_tolerance(want, weight, "bf16", 15)).all()
+    outs = [torch.full_like(alone[0], float("nan")) for _ in range(40)]
+    ws.fill_(0xFF)
+    for i, out in enumerate(outs):
+        x.call(pa, i % 2, out, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, alone[i % 2]) for i, out in enumerate(outs))
+    ws.fill_(0xFF)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(6):
+            x.call(pa, i % 2, outs[i], ws)
+    for _ in range(10):
+        for out in outs[:6]:
+            out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[i], alone[i % 2]) for i in range(6))
+
+
+def test_what_follows_a_shared_prefix_call_waits_for_it(pa, long_prefix):
+    """The next call overwrites what the prefix kernel still reads, the workspace at once: nothing of it is seen early."""
+    x = long_prefix
+    need = pa.decode_shared_prefix_workspace_bytes(60, 1, 8, 1, 128, 65536, 1100, 60)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = x.call(pa, 0, None, ws).clone()
+    k, v = x.device[0].clone(), x.device[1].clone()
+    T, D = 512, 128
+    rows = torch.full((T, 3, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int64, device="cuda")
+    table = pa.rope_table(8, D)
+    slots = [(x.tables[0, 4096 - 32:4096].long()[:, None] * 16 + torch.arange(16)).flatten().cuda()]   # the prefix's end
+    q_out = torch.empty((T, 1, D), dtype=torch.bfloat16, device="cuda")
+    for _ in range(10):
+        out = torch.empty_like(want)
+        x.device[0].copy_(k), x.device[1].copy_(v)
+        x.call(pa, 0, out, ws)
+        pa.rope_and_cache(rows[:, :1], rows[:, 1:2], rows[:, 2:], pos, table, x.device[0], x.device[1], slots[0], q_out)
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    x.device[0].copy_(k), x.device[1].copy_(v)
