@@ -323,3 +323,58 @@ def test_groups_without_a_prefix_leave_the_split_of_the_others(pa):
     rest = pa.decode(q[64:], k, v, tables[64:], lens[64:], 0.088, max_context_len=120)
     assert ((mixed[64:].float() - rest.float()).abs() <= 2.0 ** -12 + 2.0 ** -7 * rest.float().abs()).all()
     assert t_mixed < 2.5 * t_alone, (t_mixed, t_alone)
+
+
+@pytest.mark.parametrize("sizes,prefixes", [([7], [272]), ([9, 1, 0, 40, 3], [128, 0, 256, 336, 0]),
+                                            ([i % 3 for i in range(70)], [16 * (i % 9) for i in range(70)])])
+def test_generous_maxima(pa, sizes, prefixes):
+    """Upper bounds far above what the batch has, as a graph captured for any batch is given."""
+    q, k, v, tables, _, lens, gs, pl = make(sizes, prefixes, lambda b: 3 + b % 19, 2, 4, "bf16", seed=40)
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    args = [t.cuda() for t in (q, k, v, tables, lens, gs, pl)]
+    tol = ref.attention_tolerance(want, weight, "bf16", 15)
+    for mp, ms, mg in ((65536, 21, 4096), (2048, 5000, 64), (1 << 20, 40, 64)):
+        out = pa.decode_shared_prefix(*args, 0.088, max_prefix_len=mp, max_suffix_len=ms, max_group_size=mg).cpu()
+        assert ((out.double() - want).abs() <= tol).all(), (mp, ms, mg)
+
+
+@pytest.mark.expects_device_error
+@pytest.mark.parametrize("bad", [0, 31, 32, 45, 65])
+def test_a_bad_group_among_many(pa, bad):
+    """Its rows are left as they were, the others are right, and its index is reported."""
+    sizes, prefixes = [1 + i % 2 for i in range(66)], [16 * (i % 7) + 16 for i in range(66)]
+    q, k, v, tables, _, lens, gs, pl = make(sizes, prefixes, lambda b: 2 + b % 9, 1, 4, "bf16", seed=41)
+    want, weight = ref.attention(q, k, v, tables, lens, 0.088)
+    tol = ref.attention_tolerance(want, weight, "bf16", 15)
+    wrong = pl.clone()
+    wrong[bad] += 8
+    out = torch.full_like(q, 6.0).cuda()
+    pa.decode_shared_prefix(*[t.cuda() for t in (q, k, v, tables, lens, gs, wrong)], 0.088, out, max_prefix_len=128,
+                            max_suffix_len=200, max_group_size=2)
+    assert pa.get_device_error(clear=True) == (8, bad)
+    out, rows = out.cpu(), range(int(gs[bad]), int(gs[bad + 1]))
+    for b in range(len(lens)):
+        if b in rows:
+            assert (out[b] == 6.0).all()
+        else:
+            assert ((out[b].double() - want[b]).abs() <= tol[b]).all(), b
+
+
+def test_two_streams_at_once(pa):
+    """Calls that overlap, each with its own workspace: every one gives what it gives alone."""
+    work = []
+    for i, (size, prefix, suffix) in enumerate([(60, 8192, 30), (9, 20000, 2100)]):
+        q, k, v, tables, _, lens, gs, pl = make([size], [prefix], lambda b: suffix - b % 7, 2, 4, "bf16", seed=50 + i)
+        args = [t.cuda() for t in (q, k, v, tables, lens, gs, pl)]
+        maxima = dict(max_prefix_len=prefix, max_suffix_len=suffix, max_group_size=size)
+        need = pa.decode_shared_prefix_workspace_bytes(size, 1, 8, 2, 128, prefix, suffix, size)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        work.append((args, maxima, ws, pa.decode_shared_prefix(*args, 0.088, workspace=ws, **maxima), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(w[3]) for _ in range(30)] for w in work]
+    for i in range(30):
+        for (args, maxima, ws, _, stream), out in zip(work, outs):
+            pa.decode_shared_prefix(*args, 0.088, out[i], workspace=ws, stream=stream, **maxima)
+    torch.cuda.synchronize()
+    for w, out in zip(work, outs):
+        assert all(torch.equal(o, w[3]) for o in out)

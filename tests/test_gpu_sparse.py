@@ -411,3 +411,21 @@ def test_choice_of_many_long_lists(pa, ty, G, K, sink, recent):
             best = torch.sort(s, dim=1, descending=True, stable=True).indices[:, :K].sort(1).values
             want[:, :best.shape[1]] = best.int()
         assert torch.equal(got[b], want), b
+
+
+def test_bounds_of_a_block_copied_to_be_written(pa):
+    """Copy-on-write copies no bounds; the ordinary call for the token that is then written covers the copy."""
+    k, v, tables, lens = ref.make_cache([40, 40], 2, "bf16", seed=9)
+    tables[1] = tables[0]                                        # one request forked into two
+    spare = [i for i in range(k.shape[0]) if i not in tables[0].tolist()][0]
+    kd, vd = cuda(k, v)
+    bounds = torch.full((k.shape[0], 2, 2, 128), 9.0, dtype=k.dtype, device="cuda")
+    pa.update_block_bounds(kd, bounds, *cuda(tables, lens, lens))
+    pa.copy_blocks(kd, vd, torch.tensor([[int(tables[0, 2]), spare]], device="cuda"))
+    tables[1, 2] = spare
+    lens[1] = 41
+    new = torch.randn((1, 2, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda() * 3
+    pa.reshape_and_cache(new, new, kd, vd, torch.tensor([spare * 16 + 8], device="cuda"))
+    pa.update_block_bounds(kd, bounds, *cuda(tables, lens, torch.tensor([0, 1], dtype=torch.int32)))
+    want = ref.block_bounds(kd.cpu(), torch.full(bounds.shape, 9.0, dtype=k.dtype), tables, lens, lens)
+    assert torch.equal(bounds.cpu(), want)
