@@ -831,9 +831,9 @@ struct PrefixPlan {
 // CTA (one an SM) takes 8.5 of set-up and epilogue and 2.9 a step; a step is a
 // tile, or two where a CTA has at most 128 rows.  A last wave that is not full counts for
 // at least half.  Each partition's partials cost 0.35 to combine and their
-// bytes, written and read.  (47 sequences in three groups, 32 KV heads: 42.6 a call with
-// the two partitions chosen, 52.5 with one, 51.2 with three; 128 sequences over 1024 tokens:
-// 38.0 with four, 39.2 with three, 39.5 with eight; 5 over 4000: 15.9 with eight, 16.5 with
+// bytes, written and read.  (47 sequences in three groups, 32 KV heads: 44.3 a call with
+// the two partitions chosen, 55.6 with one, 53.9 with three; 128 sequences over 1024 tokens:
+// 38.0 with four, 39.2 with three, 39.5 with eight; 5 over 4000: 15.8 with eight, 16.5 with
 // sixteen, 24.6 with three.)
 int plan_part_tiles(double ctas, int tiles, bool split, double partial_us) {
   const double sms = sm_count();

@@ -12,8 +12,8 @@
 // result does not depend on which of the two products the compiler would fuse),
 // and the row is rounded once to its stored type.
 //
-// Bound by HBM: 8192 tokens of 32/8 bf16 heads (206 MB) take 32.5 us, 97% of the copy
-// bandwidth.  E4M3 caches: 4093 tokens (92 MB) 19.4 us, 73%: half the time the SMs issue
+// Bound by HBM: 8192 tokens of 32/8 bf16 heads (206 MB) take 32.5 to 33 us, 95 to 97% of the
+// copy bandwidth.  E4M3 caches: 4093 tokens (92 MB) 19.2 to 19.6 us, 73%: half the time the SMs issue
 // (rotation, quotients by the scale, conversions), and 3.5 waves of CTAs leave a tail.
 #pragma once
 
