@@ -372,7 +372,8 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
  * prefix gives an infinity or NaN (the second part of a weight may be 0).
  * Bad block ids of a prefix read as zeros (PA_DEV_BAD_BLOCK_ID).
  * Errors: as pa_decode, PA_ERR_DTYPE for other types, PA_ERR_SHAPE also for
- * num_seqs > 0 without groups, a max_prefix_len off 16 and more than 2^31 - 1 CTAs.
+ * num_seqs > 0 without groups, a max_prefix_len off 16, more than 2^24 groups or
+ * sequences a group, maxima above 2^30 and more than 2^31 - 1 CTAs.
  *
  * From what size on: neither call hands over to the other.  Measured on one B200 (us of
  * this call / of pa_decode, own tokens up to 130, caches not in L2; 32 query and 8 KV heads,

@@ -899,7 +899,7 @@ pa_status_t prefix_shape_status(int num_seqs, int num_groups, int num_heads, int
                                 int max_suffix_len, int max_group_size) {
   if (num_seqs < 0 || num_groups < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
       max_prefix_len < 0 || max_prefix_len % kBlockSize != 0 || max_suffix_len < 0 || max_group_size < 0 ||
-      max_prefix_len > (1 << 30) || max_suffix_len > (1 << 30) || max_group_size > (1 << 24))
+      max_prefix_len > (1 << 30) || max_suffix_len > (1 << 30) || max_group_size > (1 << 24) || num_groups > (1 << 24))
     return PA_ERR_SHAPE;
   const int group = num_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_SHAPE;

@@ -227,3 +227,11 @@ def test_rope_refuses_rows_that_share_columns(capi):
         assert _rope(capi, **a, qo=BIG + free + shift) == SHAPE, shift
     # other strides are compared as whole ranges
     assert _rope(capi, **{**a, "so": 5120}, qo=BIG + free) == SHAPE
+
+
+def test_shared_prefix_refuses_more_groups_than_its_loops_count(capi):
+    """The kernels walk the groups 32 at a time in 32 bits: without a bound, 2^31 - 1 groups would never end."""
+    for mp in (0, 512):
+        assert _shared(capi, n=(1 << 24) + 1, mp=mp) == SHAPE and _shared(capi, n=(1 << 31) - 1, mp=mp) == SHAPE
+    assert _shared(capi, n=1 << 24, mp=0) == WORKSPACE
+    assert capi.decode_shared_prefix_workspace_bytes(4, (1 << 24) + 1, 32, 8, 128, 0, 64, 4) == 0
